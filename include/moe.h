@@ -86,9 +86,10 @@ typedef enum { MOE_X_F32 = 0, MOE_X_BF16 = 1 } moe_xfmt;
 
 typedef enum {
   MOE_ACT_SILU = 0,     /* h = g * sigmoid(g) * u */
-  MOE_ACT_GELU_TANH = 1 /* h = g/2 * (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) * u: the
-                           moe op's other activation, 'gelu_tanh' (Kimi-Linear details
-                           page, Runtime; Qwen3 card, Conversion Notes) */
+  MOE_ACT_GELU_TANH = 1, /* h = g/2 * (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) * u: the
+                            moe op's other activation, 'gelu_tanh' (Kimi-Linear details
+                            page, Runtime; Qwen3 card, Conversion Notes) */
+  MOE_ACT_NONE = 2       /* moe_linear only: no activation (the routed layer rejects it) */
 } moe_act;
 
 typedef enum {
@@ -253,6 +254,88 @@ MOE_API moe_status moe_block_workspace_size(const moe_desc* d, const moe_shared_
 MOE_API moe_status moe_forward_block(const moe_desc* d, const moe_shared_expert* shared, const void* x, int32_t T,
                                      const int32_t* topk_idx, const float* topk_w, const void* residual, void* y,
                                      void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * The whole layer for a few tokens, in two launches: router, top k, routed
+ * experts, shared expert and residual.
+ *
+ *   y[t] = sum_j w[t,j] FFN_{idx[t,j]}(x[t])  [+ FFN_shared(x[t])]  [+ residual[t]]
+ *
+ * For the decode of 1 to MOE_FEW_MAX_TOKENS tokens, where launches and the hand-over
+ * between them cost as much as reading the experts (the pages' decode is one
+ * token at a time: Qwen3-30B-A3B LiteRT-LM card, performance table).  The formulas,
+ * layouts and formats are moe_route's, moe_forward's and moe_forward_block's; T up to
+ * MOE_FEW_MAX_TOKENS (more: MOE_ERR_UNSUPPORTED), T = 0 does nothing.
+ *   - topk_idx [T, k], topk_w [T, k]: outputs, slots in descending key order, ties to the
+ *     lower expert.  The logits are summed in 64 bits, so tokens whose border keys lie
+ *     closer than fp32 resolves may be routed otherwise than moe_route (fp32 sums) does.
+ *     Tokens with fewer than k selectable experts get idx -1 / w 0 in the unfilled slots
+ *     and raise MOE_FLAG_TOO_FEW_ACTIVE; a non-finite logit raises
+ *     MOE_FLAG_NONFINITE_LOGIT and its expert is not selectable.
+ *   - shared: NULL, or a shared expert as for moe_forward_block; its storage format must
+ *     be d->wfmt (MOE_ERR_UNSUPPORTED otherwise: use moe_route and moe_forward_block).
+ *   - residual: NULL, or [T, H] in x's format.  y may be residual itself; y, idx and w
+ *     must not overlap x.
+ *   - sums in fp32, one rounding to y's format.  The activations between the projections
+ *     are kept to at least 16 significant bits.  Results do not depend on timing: the same
+ *     call gives the same bits.
+ *   - d->path is not read.
+ * The workspace (moe_few_workspace_size bytes, 256-byte aligned) needs no initial state;
+ * calls on one stream may share it, calls that can overlap must not.  Asynchronous on
+ * `stream`, no allocation, capturable.
+ */
+#define MOE_FEW_MAX_TOKENS 16
+MOE_API moe_status moe_few_workspace_size(const moe_desc* d, const moe_shared_expert* shared, int32_t T,
+                                          size_t* bytes);
+MOE_API moe_status moe_few_forward(const moe_desc* d, const moe_shared_expert* shared, const void* x, int32_t T,
+                                   int32_t* topk_idx, float* topk_w, const void* residual, void* y,
+                                   void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * Dense matrix product with bias, activation, gate and residual in its epilogue:
+ *
+ *   v = W x + b          y = act(v) + residual                    (W_up NULL)
+ *   u = W_up x + b_up    y = act(v) * u + residual                (gated)
+ *
+ * for the dense layers beside the routed ones: the plain first layer (Kimi-Linear
+ * LiteRT-LM details page, Conversion notes: "the dense first layer in plain ops"), projections
+ * stored in the layer's formats (the same page's quantization bullet: the other linears
+ * int8 per channel), the output head.  One rounding, to y's format.
+ *
+ * moe_linear_desc: y [M, N] from x [M, K].
+ *   W, W_up: [N, K] in wfmt (int4: [N, K/2] bytes), 16-byte aligned, rows contiguous;
+ *   s, s_up: int8 [N]; int4 [N, K/32] (block 128: K/128); otherwise not read;
+ *   b, b_up: [N] fp32 or NULL (no bias); b_up is read only with W_up;
+ *   act: moe_act, MOE_ACT_NONE among them; xfmt, yfmt: moe_xfmt of x and of y and residual.
+ *   Limits: 1 <= N <= 2^24; K in [1, 65536] and a multiple of 4 (fp32 weights), 8 (bf16), 16
+ *   (int8), 32 (int4) or 128 (int4 block 128), with bf16 x of 8 at least; M <= 2^21; rows x
+ *   columns of W below 2^40.
+ * moe_linear: ldx, ldr and ldy are the distances between rows in elements (>= K, N and N):
+ *   x 16-byte aligned with rows at multiples of 16 bytes; residual (or NULL) and y aligned
+ *   to their element.  y may be residual itself (same ldr and ldy; each element is read before
+ *   it is written, by the same thread) and must not overlap x.  M = 0 does nothing.
+ *   Columns between N and ldy, and what lies behind the last row, are not touched.
+ * The workspace is as for moe_forward: moe_linear_workspace_size bytes (may be 0, then it
+ * may be NULL), 256-byte aligned, no initial state needed, shared by the calls of one
+ * stream only.  Asynchronous on `stream`, no allocation, capturable.
+ */
+typedef struct {
+  int32_t K, N;
+  int32_t act;  /* moe_act */
+  int32_t wfmt; /* moe_wfmt */
+  int32_t xfmt; /* moe_xfmt of x */
+  int32_t yfmt; /* moe_xfmt of y and residual */
+  const void* W;
+  const float* s;
+  const float* b;
+  const void* W_up; /* NULL: not gated */
+  const float* s_up;
+  const float* b_up;
+} moe_linear_desc;
+MOE_API moe_status moe_linear_workspace_size(const moe_linear_desc* d, int32_t M, size_t* bytes);
+MOE_API moe_status moe_linear(const moe_linear_desc* d, const void* x, int64_t ldx, int32_t M, const void* residual,
+                              int64_t ldr, void* y, int64_t ldy, void* workspace, size_t ws_bytes,
+                              cudaStream_t stream);
 
 /*
  * Routing statistics (CMF code specialist page, How it was made: Calibrate and

@@ -24,7 +24,8 @@ MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUD
 MOE_ROUTER_SIGMOID_BIAS, MOE_ROUTER_SOFTMAX = 0, 1
 MOE_W_F32, MOE_W_BF16, MOE_W_INT8_ROW, MOE_W_INT4_B32, MOE_W_INT4_B128 = 0, 1, 2, 3, 4
 MOE_X_F32, MOE_X_BF16 = 0, 1
-MOE_ACT_SILU, MOE_ACT_GELU_TANH = 0, 1
+MOE_ACT_SILU, MOE_ACT_GELU_TANH, MOE_ACT_NONE = 0, 1, 2
+MOE_FEW_MAX_TOKENS = 16
 MOE_PATH_AUTO, MOE_PATH_GEMV, MOE_PATH_GEMM = 0, 1, 2
 MOE_FLAG_BAD_EXPERT_INDEX, MOE_FLAG_TOO_FEW_ACTIVE, MOE_FLAG_NONFINITE_LOGIT = 1, 2, 4
 
@@ -38,7 +39,8 @@ ROUTER = {"sigmoid": MOE_ROUTER_SIGMOID_BIAS, "softmax": MOE_ROUTER_SOFTMAX}
 
 EXPORTS = ("moe_workspace_size", "moe_route", "moe_route_logits", "moe_forward", "moe_layer_forward", "moe_forward_noalloc",
            "moe_block_workspace_size",
-           "moe_forward_block", "moe_expert_counts",
+           "moe_forward_block", "moe_few_workspace_size", "moe_few_forward", "moe_linear_workspace_size", "moe_linear",
+           "moe_expert_counts",
            "moe_cover_set", "moe_selftest_bounded_wait", "moe_last_error", "moe_device_flags", "moe_launch_count",
            "moe_stage_timing", "moe_stage_times", "moe_stage_timing_only")
 
@@ -81,6 +83,13 @@ class moe_shared_expert(ctypes.Structure):
                 ("s_up", ctypes.c_void_p), ("s_down", ctypes.c_void_p)]
 
 
+class moe_linear_desc(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_int32), ("N", ctypes.c_int32), ("act", ctypes.c_int32), ("wfmt", ctypes.c_int32),
+                ("xfmt", ctypes.c_int32), ("yfmt", ctypes.c_int32), ("W", ctypes.c_void_p), ("s", ctypes.c_void_p),
+                ("b", ctypes.c_void_p), ("W_up", ctypes.c_void_p), ("s_up", ctypes.c_void_p),
+                ("b_up", ctypes.c_void_p)]
+
+
 class moe_stage_time(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 32), ("launches", ctypes.c_int32), ("total_ms", ctypes.c_float)]
 
@@ -101,6 +110,11 @@ def _load() -> ctypes.CDLL:
     SH = ctypes.POINTER(moe_shared_expert)
     lib.moe_block_workspace_size.argtypes = [D, SH, i32, ctypes.POINTER(sz)]
     lib.moe_forward_block.argtypes = [D, SH, vp, i32, vp, vp, vp, vp, vp, sz, vp]
+    lib.moe_few_workspace_size.argtypes = [D, SH, i32, ctypes.POINTER(sz)]
+    lib.moe_few_forward.argtypes = [D, SH, vp, i32, vp, vp, vp, vp, vp, sz, vp]
+    L, i64 = ctypes.POINTER(moe_linear_desc), ctypes.c_int64
+    lib.moe_linear_workspace_size.argtypes = [L, i32, ctypes.POINTER(sz)]
+    lib.moe_linear.argtypes = [L, vp, i64, i32, vp, i64, vp, i64, vp, sz, vp]
     lib.moe_expert_counts.argtypes = [D, vp, i32, vp, vp]
     lib.moe_cover_set.argtypes = [vp, i32, ctypes.c_double, vp, vp, ctypes.POINTER(i32)]
     lib.moe_selftest_bounded_wait.argtypes = [vp]
@@ -115,7 +129,8 @@ def _load() -> ctypes.CDLL:
     lib.moe_stage_timing_only.argtypes = [ctypes.c_char_p]
     for f in ("moe_workspace_size", "moe_route", "moe_route_logits", "moe_forward", "moe_layer_forward", "moe_forward_noalloc",
               "moe_block_workspace_size",
-              "moe_forward_block", "moe_expert_counts",
+              "moe_forward_block", "moe_few_workspace_size", "moe_few_forward", "moe_linear_workspace_size", "moe_linear",
+           "moe_expert_counts",
               "moe_cover_set", "moe_device_flags", "moe_stage_timing", "moe_stage_times", "moe_stage_timing_only"):
         getattr(lib, f).restype = ctypes.c_int
     return lib
@@ -190,6 +205,34 @@ def moe_forward_block(desc: moe_desc, shared: Optional["moe_shared_expert"], x: 
                                    topk_idx, topk_w, residual, y, workspace, int(ws_bytes), stream))
 
 
+def moe_few_workspace_size(desc: moe_desc, shared: Optional["moe_shared_expert"], T: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_few_workspace_size(ctypes.byref(desc), ctypes.byref(shared) if shared else None, int(T),
+                                        ctypes.byref(n)))
+    return n.value
+
+
+def moe_few_forward(desc: moe_desc, shared: Optional["moe_shared_expert"], x: int, T: int, topk_idx: int, topk_w: int,
+                    residual: Optional[int], y: int, workspace: int, ws_bytes: int, stream: int = 0) -> None:
+    """The whole layer for T <= MOE_FEW_MAX_TOKENS tokens: route, routed experts, shared
+    expert (if any) and residual (if any); topk_idx / topk_w are written."""
+    _check(lib().moe_few_forward(ctypes.byref(desc), ctypes.byref(shared) if shared else None, x, int(T), topk_idx,
+                                 topk_w, residual, y, workspace, int(ws_bytes), stream))
+
+
+def moe_linear_workspace_size(desc: moe_linear_desc, M: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_linear_workspace_size(ctypes.byref(desc), int(M), ctypes.byref(n)))
+    return n.value
+
+
+def moe_linear(desc: moe_linear_desc, x: int, ldx: int, M: int, residual: Optional[int], ldr: int, y: int, ldy: int,
+               workspace: Optional[int], ws_bytes: int, stream: int = 0) -> None:
+    """y = act(W x + b) [* (W_up x + b_up)] [+ residual], rows ldx / ldr / ldy elements apart."""
+    _check(lib().moe_linear(ctypes.byref(desc), x, int(ldx), int(M), residual, int(ldr), y, int(ldy), workspace,
+                            int(ws_bytes), stream))
+
+
 def moe_expert_counts(desc: moe_desc, topk_idx: int, T: int, counts: int, stream: int = 0) -> None:
     """counts[e] (device uint64 [E]) += entries of topk_idx [T, k] equal to e."""
     _check(lib().moe_expert_counts(ctypes.byref(desc), topk_idx, int(T), counts, stream))
@@ -248,6 +291,42 @@ def moe_stage_times() -> dict:
 
 # ---------------------------------------------------------------- convenience wrapper
 
+def _device_tensor(torch, a, device):
+    """`a` (numpy, where uint16 holds bf16 bit patterns, or a tensor) as a contiguous
+    tensor on `device`; a contiguous tensor that is there already is taken as it is."""
+    if a is None:
+        return None
+    if not isinstance(a, torch.Tensor):
+        import numpy as np
+        a = np.ascontiguousarray(a)
+        if a.dtype == np.uint16:  # bf16 bit patterns
+            a = a.view(np.int16)
+        a = torch.from_numpy(a)
+    return a.contiguous().to(device)
+
+
+def _require(ok: bool, message: str):
+    if not ok:
+        raise MoeError(MOE_ERR_INVALID_ARG, message)
+
+
+class _OnDevice:
+    """Makes `device` current for a call, where it is not already."""
+
+    def __init__(self, torch, device):
+        self.torch, self.index, self.guard = torch, device.index, None
+
+    def __enter__(self):
+        if self.index is not None and self.index != self.torch.cuda.current_device():
+            self.guard = self.torch.cuda.device(self.index)
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            guard, self.guard = self.guard, None
+            guard.__exit__(*exc)
+
+
 class MoELayer:
     """Device-resident layer: holds the weights as torch CUDA tensors, a reusable
     workspace, and calls moe_route / moe_forward on the current torch stream."""
@@ -262,15 +341,7 @@ class MoELayer:
         self.device = torch.device(device)
 
         def dev(a):
-            if a is None:
-                return None
-            if not isinstance(a, torch.Tensor):
-                import numpy as np
-                a = np.ascontiguousarray(a)
-                if a.dtype == np.uint16:  # bf16 bit patterns
-                    a = a.view(np.int16)
-                a = torch.from_numpy(a)
-            return a.contiguous().to(self.device)
+            return _device_tensor(torch, a, self.device)
 
         self.tensors = dict(W_r=dev(W_r), b=dev(b), expert_mask=dev(expert_mask), W_gate=dev(W_gate),
                             W_up=dev(W_up), W_down=dev(W_down), s_gate=dev(s_gate), s_up=dev(s_up),
@@ -299,6 +370,7 @@ class MoELayer:
             self.shared = sh
         self._bws = None
         self._bws_T = -1
+        self._few_ws = {}
 
     @property
     def x_dtype(self):
@@ -380,6 +452,45 @@ class MoELayer:
                           ws.numel(), self._stream())
         return y
 
+    def few_workspace(self, T: int, stream: int = 0):
+        """The workspace of few() calls on one stream (they run in order and share it)."""
+        ws = self._few_ws.get(stream)
+        if ws is None or ws[0] < T:
+            n = moe_few_workspace_size(self.desc, self.shared, T)
+            ws = self._few_ws[stream] = (T, self.torch.empty(max(n, 256), dtype=self.torch.uint8,
+                                                             device=self.tensors["W_r"].device))
+        return ws[1]
+
+    def few(self, x, residual=None, out=None):
+        """The whole layer for up to MOE_FEW_MAX_TOKENS tokens in two launches (moe_few_forward):
+        route, routed experts, the shared expert (if the layer has one) and residual (if
+        given, [T, H] in x's dtype).  x [T, H] contiguous; returns (y, idx, w), written into
+        `out` = (y, idx, w) if given (y may be residual itself).  Calls on one stream share a
+        workspace that the layer keeps; so do the graphs captured on one stream: replay
+        those in order, or capture them from layers of their own."""
+        torch, d = self.torch, self.desc
+        T = x.shape[0]
+        with _OnDevice(torch, x.device):
+            if out is None:
+                out = (torch.empty((T, d.H), dtype=self.x_dtype, device=x.device),
+                       torch.empty((T, d.k), dtype=torch.int32, device=x.device),
+                       torch.empty((T, d.k), dtype=torch.float32, device=x.device))
+            y, idx, w = out
+            for t, n, dtype, name in ((x, d.H, self.x_dtype, "x"), (y, d.H, self.x_dtype, "y"),
+                                      (idx, d.k, torch.int32, "idx"), (w, d.k, torch.float32, "w"),
+                                      (residual, d.H, self.x_dtype, "residual")):
+                if t is not None:
+                    _require(t.dtype == dtype and t.shape == (T, n) and t.is_contiguous() and t.device == x.device,
+                             "%s must be a contiguous %s tensor [%d, %d] on x's device" % (name, dtype, T, n))
+            _require(x.device.type == "cuda" and x.device == self.tensors["W_r"].device,
+                     "x must be on the layer's device")
+            stream = torch.cuda.current_stream(x.device).cuda_stream
+            ws = self.few_workspace(T, stream)
+            moe_few_forward(d, self.shared, x.data_ptr(), T, idx.data_ptr(), w.data_ptr(),
+                            None if residual is None else residual.data_ptr(), y.data_ptr(), ws.data_ptr(),
+                            ws.numel(), stream)
+        return y, idx, w
+
     def expert_counts(self, idx, counts=None):
         """Accumulate per-expert routing counts of idx [T, k] into counts (a device
         uint64 tensor [E], created zeroed when None) and return it."""
@@ -387,3 +498,71 @@ class MoELayer:
             counts = self.torch.zeros(self.desc.E, dtype=self.torch.uint64, device=self.device)
         moe_expert_counts(self.desc, idx.data_ptr(), idx.shape[0], counts.data_ptr(), self._stream())
         return counts
+
+
+class Linear:
+    """Device-resident dense product y = act(W x + b) [* (W_up x + b_up)] [+ residual]
+    (moe_linear): holds the weights as torch CUDA tensors and a reusable workspace, and
+    runs on the current torch stream.  W, W_up [N, K] in the storage format wfmt, scales
+    s, s_up and fp32 biases b, b_up as include/moe.h lays them out; yfmt defaults to xfmt."""
+
+    def __init__(self, *, K, N, wfmt, xfmt, W, s=None, b=None, W_up=None, s_up=None, b_up=None, act="none", yfmt=None,
+                 device="cuda"):
+        import torch
+        lib()  # fail loudly now if the CUDA library is missing
+        self.torch = torch
+        self.device = torch.device(device)
+        names = dict(ACT, none=MOE_ACT_NONE)
+        d = moe_linear_desc()
+        d.K, d.N = int(K), int(N)
+        d.act = names[act] if isinstance(act, str) else int(act)
+        d.wfmt = WFMT[wfmt] if isinstance(wfmt, str) else int(wfmt)
+        d.xfmt = XFMT[xfmt] if isinstance(xfmt, str) else int(xfmt)
+        yfmt = xfmt if yfmt is None else yfmt
+        d.yfmt = XFMT[yfmt] if isinstance(yfmt, str) else int(yfmt)
+        self.tensors = {}
+        for name, a in (("W", W), ("s", s), ("b", b), ("W_up", W_up), ("s_up", s_up), ("b_up", b_up)):
+            t = self.tensors[name] = _device_tensor(torch, a, self.device)
+            setattr(d, name, None if t is None else t.data_ptr())
+        self.desc = d
+        self.x_dtype = torch.bfloat16 if d.xfmt == MOE_X_BF16 else torch.float32
+        self.y_dtype = torch.bfloat16 if d.yfmt == MOE_X_BF16 else torch.float32
+        self._ws = {}
+
+    def workspace(self, M: int, stream: int = 0):
+        """The workspace of the calls on one stream (they run in order and share it)."""
+        n = moe_linear_workspace_size(self.desc, M)
+        ws = self._ws.get(stream)
+        if ws is None or ws.numel() < n:
+            ws = self._ws[stream] = self.torch.empty(max(n, 256), dtype=self.torch.uint8,
+                                                     device=self.tensors["W"].device)
+        return ws
+
+    def __call__(self, x, residual=None, y=None):
+        """x [M, K], rows contiguous but any (16-byte) distance apart; residual and y [M, N]
+        with contiguous rows; y may be residual itself.  Calls on one stream share a workspace
+        that the object keeps; so do the graphs captured on one stream: replay those in
+        order, or capture them from objects of their own."""
+        torch, d = self.torch, self.desc
+        M = x.shape[0]
+        with _OnDevice(torch, x.device):
+            if y is None:
+                y = torch.empty((M, d.N), dtype=self.y_dtype, device=x.device)
+            for t, n, dtype, name in ((x, d.K, self.x_dtype, "x"), (y, d.N, self.y_dtype, "y"),
+                                      (residual, d.N, self.y_dtype, "residual")):
+                if t is not None:
+                    _require(t.dtype == dtype and t.shape == (M, n) and t.device == x.device
+                             and (n == 1 or t.stride(1) == 1),
+                             "%s must be a %s tensor [%d, %d] with contiguous rows on x's device" % (name, dtype, M, n))
+            _require(x.device.type == "cuda" and x.device == self.tensors["W"].device,
+                     "x must be on the weights' device")
+
+            def ld(t, n):
+                return t.stride(0) if M > 1 else n
+
+            stream = torch.cuda.current_stream(x.device).cuda_stream
+            ws = self.workspace(M, stream)
+            moe_linear(d, x.data_ptr(), ld(x, d.K), M, None if residual is None else residual.data_ptr(),
+                       0 if residual is None else ld(residual, d.N), y.data_ptr(), ld(y, d.N), ws.data_ptr(),
+                       ws.numel(), stream)
+        return y

@@ -172,6 +172,21 @@ cudaError_t launch_expert_counts(const int32_t* idx, int64_t n, int E, uint64_t*
                                  cudaStream_t s);
 cudaError_t launch_combine(const moe_desc& d, const int32_t* idx, int T, const void* yp, bool yp_bf16, void* y,
                            cudaStream_t s, const float* ys = nullptr, const void* residual = nullptr);
+// ---- the layer for a few tokens (two launches) ----
+// counters at the start of its workspace: [0] claimed units, [kFewDone] finished gate/up
+// units, each in a 128-byte line of its own
+constexpr int kFewCounters = 64;
+constexpr int kFewDone = 32;
+size_t few_workspace_bytes(const moe_desc& d, const moe_shared_expert* sh, int T);
+cudaError_t launch_few_router(const moe_desc& d, const moe_shared_expert* sh, const void* x, int T, void* workspace,
+                              uint32_t* flags, cudaStream_t s);
+cudaError_t launch_few_layer(const moe_desc& d, const moe_shared_expert* sh, const void* x, int T, int32_t* idx,
+                             float* w, const void* residual, void* y, void* workspace, int num_sms, uint32_t* flags,
+                             cudaStream_t s);
+// ---- the dense product ----
+size_t linear_workspace_bytes(const moe_linear_desc& d, int M);
+cudaError_t launch_linear_simt(const moe_linear_desc& d, const void* x, int64_t ldx, int M, const void* residual,
+                               int64_t ldr, void* y, int64_t ldy, cudaStream_t s);
 cudaError_t launch_dense_plan(int T, int chunk, int32_t* counts, int32_t* offsets, int32_t* touched,
                               int32_t* group_base, int32_t* tile_base, int32_t* meta, int32_t* sorted_pair,
                               float* ones, cudaStream_t s);

@@ -1,0 +1,175 @@
+// Dense matrix product with its epilogue fused:
+//   v = s * (W x) + b,   y = act(v) [* v_up] + residual,
+// in fp32 with one rounding to y's format.  Weights in the layer's storage formats.
+//
+// A CTA computes 64 tokens x 64 outputs from 16-column slices of x and W held in shared
+// memory as fp32 (weights decoded on the way in), 4 x 4 sums per thread.
+#include "common.cuh"
+#include "internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int kTile = 64;
+constexpr int kSlice = 16;
+
+struct LinearArgs {
+  int M, N, K;
+  int act;
+  const void* x;
+  long long ldx;
+  const void* W[2];  // W, W_up
+  const float* s[2];
+  const float* b[2];
+  const void* residual;
+  long long ldr;
+  void* y;
+  long long ldy;
+};
+
+__device__ __forceinline__ float activate(float v, int act) {
+  if (act == MOE_ACT_SILU) return silu_mul(v, 1.f);
+  if (act == MOE_ACT_GELU_TANH) return gelu_tanh_mul(v, 1.f);
+  return v;
+}
+
+// four stored weights of row r from column c on (c a multiple of 4)
+template <int WF>
+__device__ __forceinline__ void weights4(const void* W, const float* s, size_t r, int c, int K, float (&v)[4]) {
+  if constexpr (WF == MOE_W_F32) {
+    const float4 u = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(W) + r * K + c));
+    v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+  } else if constexpr (WF == MOE_W_BF16) {
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(W) + r * K + c));
+    v[0] = bf16_to_f32(u.x & 0xFFFFu), v[1] = __uint_as_float(u.x & 0xFFFF0000u);
+    v[2] = bf16_to_f32(u.y & 0xFFFFu), v[3] = __uint_as_float(u.y & 0xFFFF0000u);
+  } else if constexpr (WF == MOE_W_INT8_ROW) {
+    const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const int8_t*>(W) + r * K + c));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = (float)(int8_t)(u >> (8 * j));
+  } else {
+    constexpr int kShift = WF == MOE_W_INT4_B32 ? 5 : 7;
+    const uint32_t u = __ldg(reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(W) + (r * K + c) / 2));
+    const float scale = __ldg(s + r * (K >> kShift) + (c >> kShift));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = (float)((int)(u << (28 - 4 * j)) >> 28) * scale;
+  }
+}
+
+template <int WF, int XF, int YF, bool GATED>
+__global__ void __launch_bounds__(256) linear_simt_kernel(const LinearArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int G = GATED ? 2 : 1;
+  __shared__ float xs[kSlice][kTile + 4];
+  __shared__ float ws[G][kSlice][kTile + 4];
+  const int tid = threadIdx.x;
+  const int n0 = blockIdx.x * kTile, m0 = blockIdx.y * kTile;
+  const int tn = (tid & 15) * 4, tm = (tid >> 4) * 4;
+  float acc[G][4][4] = {};
+  for (int k0 = 0; k0 < a.K; k0 += kSlice) {
+    const int r = tid >> 2, c = (tid & 3) * 4;
+    float v[4] = {};
+    if (m0 + r < a.M && k0 + c < a.K) {
+      const size_t at = (size_t)(m0 + r) * a.ldx + k0 + c;
+      if constexpr (XF == MOE_X_F32) {
+        const float4 u = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.x) + at));
+        v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+      } else {
+        const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.x) + at));
+        v[0] = bf16_to_f32(u.x & 0xFFFFu), v[1] = __uint_as_float(u.x & 0xFFFF0000u);
+        v[2] = bf16_to_f32(u.y & 0xFFFFu), v[3] = __uint_as_float(u.y & 0xFFFF0000u);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) xs[c + j][r] = v[j];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      float q[4] = {};
+      if (n0 + r < a.N && k0 + c < a.K) weights4<WF>(a.W[g], a.s[g], (size_t)(n0 + r), k0 + c, a.K, q);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ws[g][c + j][r] = q[j];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int kk = 0; kk < kSlice; ++kk) {
+      const float4 xv = *reinterpret_cast<const float4*>(&xs[kk][tm]);
+      const float xa[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const float4 wv = *reinterpret_cast<const float4*>(&ws[g][kk][tn]);
+        const float wa[4] = {wv.x, wv.y, wv.z, wv.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[g][i][j] = fmaf(xa[i], wa[j], acc[g][i][j]);
+      }
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int n = n0 + tn + j;
+    if (n >= a.N) break;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int m = m0 + tm + i;
+      if (m >= a.M) break;
+      float v[G];
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        v[g] = acc[g][i][j];
+        if constexpr (WF == MOE_W_INT8_ROW) v[g] *= a.s[g][n];
+        if (a.b[g]) v[g] += a.b[g][n];
+      }
+      float y = activate(v[0], a.act);
+      if constexpr (GATED) y *= v[G - 1];
+      if constexpr (YF == MOE_X_F32) {
+        if (a.residual) y += static_cast<const float*>(a.residual)[(size_t)m * a.ldr + n];
+        static_cast<float*>(a.y)[(size_t)m * a.ldy + n] = y;
+      } else {
+        if (a.residual) y += bf16_to_f32(static_cast<const uint16_t*>(a.residual)[(size_t)m * a.ldr + n]);
+        static_cast<uint16_t*>(a.y)[(size_t)m * a.ldy + n] = f32_to_bf16(y);
+      }
+    }
+  }
+}
+
+template <int WF, int XF, int YF>
+cudaError_t launch_simt(const LinearArgs& a, cudaStream_t s) {
+  const dim3 grid((a.N + kTile - 1) / kTile, (a.M + kTile - 1) / kTile), block(256);
+  return a.W[1] ? launch_k(linear_simt_kernel<WF, XF, YF, true>, grid, block, 0, s, a)
+                : launch_k(linear_simt_kernel<WF, XF, YF, false>, grid, block, 0, s, a);
+}
+
+template <int WF>
+cudaError_t launch_simt(const moe_linear_desc& d, const LinearArgs& a, cudaStream_t s) {
+  if (d.xfmt == MOE_X_F32)
+    return d.yfmt == MOE_X_F32 ? launch_simt<WF, MOE_X_F32, MOE_X_F32>(a, s) : launch_simt<WF, MOE_X_F32, MOE_X_BF16>(a, s);
+  return d.yfmt == MOE_X_F32 ? launch_simt<WF, MOE_X_BF16, MOE_X_F32>(a, s) : launch_simt<WF, MOE_X_BF16, MOE_X_BF16>(a, s);
+}
+
+}  // namespace
+
+size_t linear_workspace_bytes(const moe_linear_desc& d, int M) {
+  (void)d;
+  (void)M;
+  return 0;
+}
+
+cudaError_t launch_linear_simt(const moe_linear_desc& d, const void* x, int64_t ldx, int M, const void* residual,
+                               int64_t ldr, void* y, int64_t ldy, cudaStream_t s) {
+  LinearArgs a = {};
+  a.M = M, a.N = d.N, a.K = d.K, a.act = d.act;
+  a.x = x, a.ldx = ldx, a.residual = residual, a.ldr = ldr, a.y = y, a.ldy = ldy;
+  a.W[0] = d.W, a.W[1] = d.W_up, a.s[0] = d.s, a.s[1] = d.s_up, a.b[0] = d.b, a.b[1] = d.b_up;
+  switch (d.wfmt) {
+    case MOE_W_F32: return launch_simt<MOE_W_F32>(d, a, s);
+    case MOE_W_BF16: return launch_simt<MOE_W_BF16>(d, a, s);
+    case MOE_W_INT8_ROW: return launch_simt<MOE_W_INT8_ROW>(d, a, s);
+    case MOE_W_INT4_B32: return launch_simt<MOE_W_INT4_B32>(d, a, s);
+    default: return launch_simt<MOE_W_INT4_B128>(d, a, s);
+  }
+}
+
+}  // namespace moe

@@ -588,6 +588,120 @@ extern "C" moe_status moe_forward_block(const moe_desc* d, const moe_shared_expe
   return MOE_OK;
 }
 
+// ------------------------------------------------------------------ the layer for a few tokens
+
+static moe_status validate_few(const moe_desc* d, const moe_shared_expert* shared, int32_t T) {
+  moe_status st = validate_desc(d);
+  if (st != MOE_OK) return st;
+  if ((st = validate_T(T, d->k)) != MOE_OK) return st;
+  if (T > MOE_FEW_MAX_TOKENS)
+    return fail(MOE_ERR_UNSUPPORTED, "at most %d tokens (got %d): use moe_layer_forward or moe_forward_block",
+                MOE_FEW_MAX_TOKENS, T);
+  if ((st = validate_shared(*d, shared)) != MOE_OK) return st;
+  if (shared && shared->wfmt != d->wfmt)
+    return fail(MOE_ERR_UNSUPPORTED, "the shared expert's storage format must be the routed experts' (got %d and %d)",
+                shared->wfmt, d->wfmt);
+  return MOE_OK;
+}
+
+extern "C" moe_status moe_few_workspace_size(const moe_desc* d, const moe_shared_expert* shared, int32_t T,
+                                             size_t* bytes) {
+  g_err.clear();
+  moe_status st = validate_few(d, shared, T);
+  if (st != MOE_OK) return st;
+  if (!bytes) return fail(MOE_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = few_workspace_bytes(*d, shared, T);
+  return MOE_OK;
+}
+
+// a workspace of `need` bytes, or the status that refuses it
+static moe_status check_scratch(const void* ws, size_t ws_bytes, size_t need) {
+  if (need == 0) return MOE_OK;
+  if (!ws) return fail(MOE_ERR_WORKSPACE, "workspace is NULL (need %zu bytes)", need);
+  if (!aligned(ws, 256)) return fail(MOE_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  if (ws_bytes < need) return fail(MOE_ERR_WORKSPACE, "workspace too small: %zu bytes given, %zu needed", ws_bytes, need);
+  return MOE_OK;
+}
+
+extern "C" moe_status moe_few_forward(const moe_desc* d, const moe_shared_expert* shared, const void* x, int32_t T,
+                                      int32_t* topk_idx, float* topk_w, const void* residual, void* y,
+                                      void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  g_err.clear();
+  moe_status st = validate_few(d, shared, T);
+  if (st != MOE_OK) return st;
+  if (T == 0) return MOE_OK;
+  if ((st = check_io(x, y, topk_idx, topk_w)) != MOE_OK) return st;
+  if (residual && !aligned(residual, 16)) return fail(MOE_ERR_INVALID_ARG, "residual must be 16-byte aligned");
+  if ((st = check_scratch(workspace, ws_bytes, few_workspace_bytes(*d, shared, T))) != MOE_OK) return st;
+  DeviceState* dev = nullptr;
+  if ((st = device_state(&dev)) != MOE_OK) return st;
+  MOE_LAUNCH("few_router", stream, launch_few_router(*d, shared, x, T, workspace, dev->flags, stream));
+  MOE_LAUNCH("few_layer", stream,
+             launch_few_layer(*d, shared, x, T, topk_idx, topk_w, residual, y, workspace, dev->num_sms, dev->flags,
+                              stream));
+  return MOE_OK;
+}
+
+// ------------------------------------------------------------------ the dense product
+
+static moe_status validate_linear(const moe_linear_desc* d, int32_t M) {
+  if (!d) return fail(MOE_ERR_INVALID_ARG, "desc is NULL");
+  if (d->K <= 0 || d->N <= 0) return fail(MOE_ERR_INVALID_ARG, "K and N must be positive (got %d, %d)", d->K, d->N);
+  if (d->wfmt < MOE_W_F32 || d->wfmt > MOE_W_INT4_B128) return fail(MOE_ERR_INVALID_ARG, "unknown weight format %d", d->wfmt);
+  if (d->xfmt != MOE_X_F32 && d->xfmt != MOE_X_BF16) return fail(MOE_ERR_INVALID_ARG, "unknown x dtype %d", d->xfmt);
+  if (d->yfmt != MOE_X_F32 && d->yfmt != MOE_X_BF16) return fail(MOE_ERR_INVALID_ARG, "unknown y dtype %d", d->yfmt);
+  if (d->act != MOE_ACT_NONE && d->act != MOE_ACT_SILU && d->act != MOE_ACT_GELU_TANH)
+    return fail(MOE_ERR_INVALID_ARG, "unknown activation %d", d->act);
+  static const int kStep[5] = {4, 8, 16, 32, 128};  // by wfmt
+  const int step = std::max(kStep[d->wfmt], d->xfmt == MOE_X_BF16 ? 8 : 4);
+  if (d->K % step) return fail(MOE_ERR_INVALID_ARG, "K must be a multiple of %d for these formats (got %d)", step, d->K);
+  if (d->K > 65536) return fail(MOE_ERR_UNSUPPORTED, "K is limited to 65536 (got %d)", d->K);
+  if (d->N > 1 << 24) return fail(MOE_ERR_UNSUPPORTED, "N is limited to 2^24 (got %d)", d->N);
+  if (M < 0) return fail(MOE_ERR_INVALID_ARG, "M must be >= 0 (got %d)", M);
+  if (M > 1 << 21) return fail(MOE_ERR_UNSUPPORTED, "M is limited to 2^21 (got %d)", M);
+  if (!d->W || !aligned(d->W, 16) || !aligned(d->W_up, 16))
+    return fail(MOE_ERR_INVALID_ARG, "W must be non-NULL, W and W_up 16-byte aligned");
+  const bool scaled = d->wfmt != MOE_W_F32 && d->wfmt != MOE_W_BF16;
+  if (scaled && (!d->s || (d->W_up && !d->s_up))) return fail(MOE_ERR_INVALID_ARG, "int8/int4 weights need their scales");
+  if (!aligned(d->s, 4) || !aligned(d->s_up, 4) || !aligned(d->b, 4) || !aligned(d->b_up, 4))
+    return fail(MOE_ERR_INVALID_ARG, "scales and biases must be 4-byte aligned");
+  return MOE_OK;
+}
+
+extern "C" moe_status moe_linear_workspace_size(const moe_linear_desc* d, int32_t M, size_t* bytes) {
+  g_err.clear();
+  moe_status st = validate_linear(d, M);
+  if (st != MOE_OK) return st;
+  if (!bytes) return fail(MOE_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = linear_workspace_bytes(*d, M);
+  return MOE_OK;
+}
+
+extern "C" moe_status moe_linear(const moe_linear_desc* d, const void* x, int64_t ldx, int32_t M,
+                                 const void* residual, int64_t ldr, void* y, int64_t ldy, void* workspace,
+                                 size_t ws_bytes, cudaStream_t stream) {
+  g_err.clear();
+  moe_status st = validate_linear(d, M);
+  if (st != MOE_OK) return st;
+  if (M == 0) return MOE_OK;
+  const int xb = d->xfmt == MOE_X_F32 ? 4 : 2, yb = d->yfmt == MOE_X_F32 ? 4 : 2;
+  constexpr int64_t kMaxLd = (int64_t)1 << 32;
+  if (!x || !aligned(x, 16)) return fail(MOE_ERR_INVALID_ARG, "x must be a non-NULL 16-byte aligned device pointer");
+  if (ldx < d->K || ldx > kMaxLd || (ldx * xb) % 16)
+    return fail(MOE_ERR_INVALID_ARG, "ldx must be >= K and rows of x 16-byte aligned (got %lld)", (long long)ldx);
+  if (!y || !aligned(y, yb)) return fail(MOE_ERR_INVALID_ARG, "y must be a non-NULL device pointer aligned to its element");
+  if (ldy < d->N || ldy > kMaxLd) return fail(MOE_ERR_INVALID_ARG, "ldy must be >= N (got %lld)", (long long)ldy);
+  if (residual && (!aligned(residual, yb) || ldr < d->N || ldr > kMaxLd))
+    return fail(MOE_ERR_INVALID_ARG, "residual must be aligned to its element and ldr >= N (got %lld)", (long long)ldr);
+  if (residual == y && ldr != ldy)
+    return fail(MOE_ERR_INVALID_ARG, "an in-place residual needs ldr == ldy (got %lld, %lld)", (long long)ldr, (long long)ldy);
+  if ((st = check_scratch(workspace, ws_bytes, linear_workspace_bytes(*d, M))) != MOE_OK) return st;
+  DeviceState* dev = nullptr;
+  if ((st = device_state(&dev)) != MOE_OK) return st;
+  MOE_LAUNCH("linear_simt", stream, launch_linear_simt(*d, x, ldx, M, residual, ldr, y, ldy, stream));
+  return MOE_OK;
+}
+
 // ------------------------------------------------------------------ routing statistics
 
 extern "C" moe_status moe_expert_counts(const moe_desc* d, const int32_t* topk_idx, int32_t T, uint64_t* counts,

@@ -10,6 +10,7 @@ if ROOT not in sys.path:
 
 def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs a CUDA device (B200, sm_100a)")
+    config.addinivalue_line("markers", "flags: raises device data flags on purpose")
     config.addinivalue_line("markers", "slow: long-running CPU case")
 
 
