@@ -14,14 +14,17 @@
 // are running and do not wait themselves: the wait ends however many CTAs are resident and
 // whatever else runs on the GPU.  It is bounded in time all the same (MOE_FLAG_TIMEOUT).
 // The router launch zeroes the counters, so the workspace needs no initial state.
+#include <type_traits>
+
 #include "common.cuh"
 #include "internal.h"
+#include "stream_dev.cuh"
+#include "tmap.h"
 
 namespace moe {
 namespace {
 
-constexpr int kRouterThreads = 128;
-constexpr int kRouterTokens = 4;  // tokens per pass over a router row
+constexpr int kRouterThreads = 256;
 
 // order-preserving image of a key: larger key, larger integer; 0 is kept for "not selectable"
 __device__ __forceinline__ uint64_t sortable(double key) {
@@ -41,57 +44,61 @@ __device__ __forceinline__ void load4(const void* base, size_t i, float (&v)[4])
   }
 }
 
-// One CTA per expert.
+// One CTA per expert.  Its warps share out the tokens, or, where there are fewer tokens than
+// warps, `split` warps share a token's columns; a lane keeps four 16-byte loads of the
+// router row in flight.
 template <int XF>
 __global__ void __launch_bounds__(kRouterThreads)
     few_router_kernel(const void* __restrict__ x, const float* __restrict__ W_r, const float* __restrict__ bias,
-                      const uint8_t* __restrict__ mask, int T, int H, int E, int router, uint64_t* __restrict__ keys,
-                      double* __restrict__ scores, uint32_t* __restrict__ counters, uint32_t* flags) {
+                      const uint8_t* __restrict__ mask, int T, int H, int E, int router, int split,
+                      uint64_t* __restrict__ keys, double* __restrict__ scores, uint32_t* __restrict__ counters,
+                      uint32_t* flags) {
   pdl_wait();
   pdl_trigger();
-  __shared__ double part[kRouterThreads / 32][kRouterTokens];
-  const int e = blockIdx.x, tid = threadIdx.x;
+  __shared__ double part[MOE_FEW_MAX_TOKENS][kRouterThreads / 32];
+  const int e = blockIdx.x, tid = threadIdx.x, w = warp_id(), lane = lane_id();
   if (e == 0 && tid < kFewCounters) counters[tid] = 0;
   const float* row = W_r + (size_t)e * H;
-  for (int t0 = 0; t0 < T; t0 += kRouterTokens) {
-    double acc[kRouterTokens] = {};
-    for (int c = tid * 4; c < H; c += kRouterThreads * 4) {
-      float w[4];
-      load4<MOE_X_F32>(row, c, w);
+  const int share = w % split, step = split * 128;
+  for (int t = w / split; t < T; t += (kRouterThreads / 32) / split) {
+    double acc[4] = {0.0, 0.0, 0.0, 0.0};
+    for (int c0 = share * 128 + lane * 4; c0 < H; c0 += 4 * step) {
+      float r[4][4], v[4][4];
 #pragma unroll
-      for (int j = 0; j < kRouterTokens; ++j) {
-        if (t0 + j >= T) break;
-        float v[4];
-        load4<XF>(x, (size_t)(t0 + j) * H + c, v);
+      for (int j = 0; j < 4; ++j) {
+        const int c = c0 + j * step;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) acc[j] = fma((double)w[q], (double)v[q], acc[j]);
+        for (int q = 0; q < 4; ++q) r[j][q] = v[j][q] = 0.f;
+        if (c < H) {
+          load4<MOE_X_F32>(row, c, r[j]);
+          load4<XF>(x, (size_t)t * H + c, v[j]);
+        }
       }
-    }
 #pragma unroll
-    for (int j = 0; j < kRouterTokens; ++j) {
-      if (t0 + j >= T) break;
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) acc[j] += __shfl_xor_sync(0xFFFFFFFFu, acc[j], off);
-      if (lane_id() == 0) part[warp_id()][j] = acc[j];
+        for (int q = 0; q < 4; ++q) acc[q] = fma((double)r[j][q], (double)v[j][q], acc[q]);
     }
-    __syncthreads();
-    const int t = t0 + tid;
-    if (tid < kRouterTokens && t < T) {
-      double l = 0.0;
+    double l = (acc[0] + acc[1]) + (acc[2] + acc[3]);
 #pragma unroll
-      for (int w = 0; w < kRouterThreads / 32; ++w) l += part[w][tid];
-      const bool finite = isfinite((float)l);
-      if (!finite) raise_flag(flags, MOE_FLAG_NONFINITE_LOGIT);
-      double score = l, key = l;
-      if (router == MOE_ROUTER_SIGMOID_BIAS) {
-        score = 1.0 / (1.0 + exp(-l));
-        key = score + (bias ? (double)bias[e] : 0.0);
-      }
-      const bool open = finite && key == key && (mask == nullptr || mask[e] != 0);
-      keys[(size_t)t * E + e] = open ? sortable(key) : 0;
-      scores[(size_t)t * E + e] = score;
+    for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, off);
+    if (lane == 0) part[t][share] = l;
+  }
+  __syncthreads();
+  if (tid < T) {
+    const int t = tid;
+    double l = 0.0;
+    for (int s = 0; s < split; ++s) l += part[t][s];
+    const bool finite = isfinite((float)l);
+    if (!finite) raise_flag(flags, MOE_FLAG_NONFINITE_LOGIT);
+    double score = l, key = l;
+    if (router == MOE_ROUTER_SIGMOID_BIAS) {
+      score = 1.0 / (1.0 + exp(-l));
+      key = score + (bias ? (double)bias[e] : 0.0);
     }
-    __syncthreads();
+    const bool open = finite && key == key && (mask == nullptr || mask[e] != 0);
+    keys[(size_t)t * E + e] = open ? sortable(key) : 0;
+    scores[(size_t)t * E + e] = score;
   }
 }
 
@@ -108,6 +115,11 @@ struct FewArgs {
   const uint64_t* keys;
   const double* scores;
   float* h;           // [T k, I] of the routed pairs, then [T, Is] of the shared expert
+  uint16_t* h2;       // the same in two bf16 planes (value and remainder) on the streaming path
+  size_t plane;       // elements of a plane
+  // int4 block scales come with the weights as boxes, per matrix, or are read where they
+  // lie: [0] routed gate/up, [1] routed down, [2], [3] shared
+  uint8_t boxed[4];
   uint32_t* counters; // [0] claimed units, [kFewDone] finished gate/up units
   int32_t* idx;
   float* w;
@@ -115,11 +127,12 @@ struct FewArgs {
   uint32_t* flags;
 };
 
-// Top k of one token by one warp, from keys held PER_LANE to a lane (expert lane + 32 j):
-// k rounds of a warp-wide maximum over the 64-bit keys, upper halves first, then lower
-// halves, ties to the lower expert.
+// The k best experts of one token by one warp, from keys held PER_LANE to a lane (expert lane +
+// 32 j): k rounds of a warp-wide maximum over the lanes' best keys, by their upper halves
+// and, only where those are equal, the lower halves and then the expert's number.  Lane
+// `slot` returns its expert, -1 where none is left.
 template <int PER_LANE>
-__device__ __forceinline__ void few_topk(const FewArgs& a, int t, int* out_e, float* out_w, bool write) {
+__device__ __forceinline__ int few_topk(const FewArgs& a, int t) {
   const int lane = lane_id();
   uint64_t key[PER_LANE];
 #pragma unroll
@@ -128,45 +141,61 @@ __device__ __forceinline__ void few_topk(const FewArgs& a, int t, int* out_e, fl
     key[j] = e < a.E ? a.keys[(size_t)t * a.E + e] : 0;
   }
   int mine = -1;
-  for (int slot = 0; slot < a.k; ++slot) {
-    uint64_t best = 0;
-    int bj = 0;
+  uint64_t best = 0;
+  int bj = 0;
+  auto find = [&] {
+    best = 0;
 #pragma unroll
     for (int j = 0; j < PER_LANE; ++j)
       if (key[j] > best) best = key[j], bj = j;
+  };
+  find();
+  for (int slot = 0; slot < a.k; ++slot) {
     const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(best >> 32));
-    const bool in = best != 0 && (uint32_t)(best >> 32) == hi;
-    const uint32_t lo = __reduce_max_sync(0xFFFFFFFFu, in ? (uint32_t)best : 0u);
-    const bool win = in && (uint32_t)best == lo;
-    const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, win ? (uint32_t)(lane + 32 * bj) : 0xFFFFFFFFu);
-    if (e == 0xFFFFFFFFu) {
-      if (write && lane == 0) raise_flag(a.flags, MOE_FLAG_TOO_FEW_ACTIVE);
-      break;
+    uint32_t who = __ballot_sync(0xFFFFFFFFu, best != 0 && (uint32_t)(best >> 32) == hi);
+    if (who == 0) break;
+    if (who & (who - 1)) {
+      const bool in = (who >> lane) & 1u;
+      const uint32_t lo = __reduce_max_sync(0xFFFFFFFFu, in ? (uint32_t)best : 0u);
+      const bool win = in && (uint32_t)best == lo;
+      const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, win ? (uint32_t)(lane + 32 * bj) : 0xFFFFFFFFu);
+      who = 1u << (e & 31u);
     }
-    if ((int)(e & 31u) == lane) {
+    const int from = __ffs(who) - 1;
+    const int e = __shfl_sync(0xFFFFFFFFu, lane + 32 * bj, from);
+    if (lane == from) {
 #pragma unroll
       for (int j = 0; j < PER_LANE; ++j)
-        if (j == (int)(e >> 5)) key[j] = 0;
+        if (j == bj) key[j] = 0;
+      find();
     }
-    if (lane == slot) mine = (int)e;
+    if (lane == slot) mine = e;
   }
-  // the chosen scores, renormalised (softmax: relative to the best logit, which the full
-  // denominator cancels against)
-  const double score = mine >= 0 ? a.scores[(size_t)t * a.E + mine] : 0.0;
+  return mine;
+}
+
+__device__ __forceinline__ int few_topk(const FewArgs& a, int t) {
+  return a.E <= 256 ? few_topk<8>(a, t) : few_topk<32>(a, t);
+}
+
+// The weight of lane `slot`'s expert: the chosen scores renormalised (softmax: relative to the
+// best logit, which the full denominator cancels against).  The whole warp calls it.
+__device__ __forceinline__ float few_weight(const FewArgs& a, int t, int e) {
+  const double score = e >= 0 ? a.scores[(size_t)t * a.E + e] : 0.0;
   const double top = __shfl_sync(0xFFFFFFFFu, score, 0);
-  const double v = mine < 0 ? 0.0 : (a.router == MOE_ROUTER_SIGMOID_BIAS ? score : exp(score - top));
+  const double v = e < 0 ? 0.0 : (a.router == MOE_ROUTER_SIGMOID_BIAS ? score : exp(score - top));
   double total = v;
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, off);
-  if (lane < a.k) {
-    const float w = (mine >= 0 && total > 0.0) ? (float)(v / total * (double)a.scale) : 0.f;
-    out_e[t * a.k + lane] = mine;
-    out_w[t * a.k + lane] = w;
-    if (write) {
-      a.idx[t * a.k + lane] = mine;
-      a.w[t * a.k + lane] = w;
-    }
-  }
+  return (e >= 0 && total > 0.0) ? (float)(v / total * (double)a.scale) : 0.f;
+}
+
+// one CTA writes the routing out
+__device__ __forceinline__ void few_write_route(const FewArgs& a, int t, int e, float w) {
+  if (lane_id() >= a.k) return;
+  a.idx[t * a.k + lane_id()] = e;
+  a.w[t * a.k + lane_id()] = w;
+  if (e < 0) raise_flag(a.flags, MOE_FLAG_TOO_FEW_ACTIVE);
 }
 
 // lane's share of sum_c W[c] v[c] over one stored row; lanes take 8 columns in turn
@@ -229,8 +258,10 @@ __global__ void __launch_bounds__(kFewThreads) few_layer_kernel(const FewArgs a)
   const int warp = warp_id(), lane = lane_id();
   if (threadIdx.x == 0) dead = 0;
   for (int t = warp; t < a.T; t += kFewThreads / 32) {
-    if (a.E <= 256) few_topk<8>(a, t, pair_e, pair_w, blockIdx.x == 0);
-    else few_topk<32>(a, t, pair_e, pair_w, blockIdx.x == 0);
+    const int e = few_topk(a, t);
+    const float wt = few_weight(a, t, e);
+    if (lane < a.k) pair_e[t * a.k + lane] = e, pair_w[t * a.k + lane] = wt;
+    if (blockIdx.x == 0) few_write_route(a, t, e, wt);
   }
   const int P = a.T * a.k;
   const uint32_t ub = (uint32_t)(a.I / kFewRows), us = (uint32_t)(a.Is / kFewRows), hb = (uint32_t)(a.H / kFewRows);
@@ -317,6 +348,484 @@ __global__ void __launch_bounds__(kFewThreads) few_layer_kernel(const FewArgs a)
   }
 }
 
+// ------------------------------------------------------------------ the streaming kernel
+//
+// bf16 tokens on bf16, int8 or int4 weights.  One persistent CTA per SM, twelve equal warps.
+// A gate/up unit is 16 rows of W_gate and the same 16 of W_up of one expert for up to 8 of its
+// tokens: both projections of an output end up in one lane.  The unit's reduction is shared
+// out over the warps box by box (16 rows x 128 bytes), so that a unit streams at the whole
+// SM's rate; each warp copies its boxes into a ring of its own by TMA, several stages
+// ahead and across units, and needs no other warp for that.  The warps' sums meet in shared
+// memory; the warp whose share of the unit is smallest adds them up, applies the activation
+// and stores h.  (One copying, one summing and ten multiplying warps measured worse: the
+// summing warp, all latency, held up the rest.)
+// After a barrier over the grid a CTA computes 16 rows of y for every chosen expert (and the
+// shared one), one after the other, so the combine stays inside the CTA.  Down weights do not
+// depend on h: the rings are full of them before the barrier opens.  h is handed over as
+// bf16 value plus bf16 remainder (16 significant bits): the remainder takes token columns of
+// the matrix instruction that would be empty, where a rounded h would add an error as large
+// as y's own rounding.  What is summed together depends on the plan alone, so the same call
+// gives the same bits.
+
+constexpr int kWarps = 12;
+constexpr int kStreamThreads = 32 * kWarps;
+constexpr int kMaxPairs = MOE_FEW_MAX_TOKENS * 32;
+constexpr int kUpTokens = 8;    // tokens of a gate/up unit
+constexpr int kDownTokens = 4;  // tokens of a down tile: values in columns 0..3, remainders in 4..7
+constexpr int kMaxStages = 4;
+
+template <int WF>
+struct Ring {
+  using F = stream::Format<WF>;
+  static constexpr int kStage = 2 * (stream::kBoxBytes + F::kScaleBox);  // gate and up box, or down boxes
+  static constexpr int kDownBoxes = F::kInt4 ? 1 : 2;                    // of a stage (bounds the tokens loaded ahead)
+  static constexpr int kStages = F::kScaleBoxes ? 3 : kMaxStages;
+  static constexpr int kBytes = kWarps * kStages * kStage;
+};
+
+struct FewMaps {
+  CUtensorMap w[3], ws[3];  // gate, up, down of the routed experts and of the shared one
+  CUtensorMap s[3], ss[3];  // their int4 block-32 scales, where `boxed` says so
+};
+
+// A group of tokens of one expert, packed: expert (or kSharedEntry), first sorted pair (shared:
+// first token), tokens.
+constexpr uint32_t kSharedEntry = 1024;
+__device__ __forceinline__ uint32_t pack_entry(uint32_t e, int start, int n) {
+  return e | (uint32_t)start << 11 | (uint32_t)n << 21;
+}
+__device__ __forceinline__ uint32_t entry_e(uint32_t v) { return v & 2047u; }
+__device__ __forceinline__ int entry_start(uint32_t v) { return (int)(v >> 11 & 1023u); }
+__device__ __forceinline__ int entry_n(uint32_t v) { return (int)(v >> 21); }
+
+struct StreamShared {
+  uint64_t full[kWarps][kMaxStages];
+  uint64_t rfull[2], rempty[2];  // the warps' sums of a unit written / added up
+  int n_up, n_down;              // entries
+  float pair_w[kMaxPairs];
+  int16_t pair[kMaxPairs];       // valid pairs in expert order
+  uint32_t up[kMaxPairs + 2], down[kMaxPairs + 4];  // entries: shared first / shared last
+  union {
+    float4 part[2][kWarps][2][32];             // [unit parity][share][gate, up]
+    float y[kWarps][MOE_FEW_MAX_TOKENS][16];   // down: each warp's share of 16 rows
+    struct {
+      int e[kMaxPairs];                        // building the plan: by pair
+      int by_rank[kMaxPairs];                  // in expert order: expert, -1 at the end
+      int place[kMaxPairs];                    //   place among the expert's pairs << 16 | their number
+    } plan;
+  };
+};
+
+__device__ __forceinline__ void few_wait(uint64_t* bar, uint32_t parity, bool& dead, uint32_t* flags) {
+  if (dead) return;
+  if (!mbar_wait(bar, parity)) {
+    dead = true;
+    raise_flag(flags, MOE_FLAG_TIMEOUT);
+  }
+}
+
+// Entries of at most `most` tokens from the sorted pairs, appended from list[n] on by one warp.
+__device__ __forceinline__ int list_entries(const StreamShared& sh, int P, int most, uint32_t* list, int n) {
+  const int lane = lane_id();
+  for (int r0 = 0; r0 < P; r0 += 32) {
+    const int r = r0 + lane;
+    const int e = r < P ? sh.plan.by_rank[r] : -1;
+    const int at = e >= 0 ? sh.plan.place[r] >> 16 : 0, of = e >= 0 ? sh.plan.place[r] & 0xFFFF : 0;
+    const bool head = e >= 0 && at % most == 0;
+    const uint32_t heads = __ballot_sync(0xFFFFFFFFu, head);
+    if (head) list[n + __popc(heads & ((1u << lane) - 1u))] = pack_entry((uint32_t)e, r, min(most, of - at));
+    n += __popc(heads);
+  }
+  return n;
+}
+
+template <int WF>
+__global__ void __launch_bounds__(kStreamThreads, 1)
+    few_stream_kernel(const __grid_constant__ FewMaps maps, const __grid_constant__ FewArgs a) {
+  using R = Ring<WF>;
+  using F = stream::Format<WF>;
+  extern __shared__ uint8_t smem[];
+  // the rings first, on 1,024 bytes (the swizzle's period)
+  uint8_t* rings = smem + (((smem_u32(smem) + 1023u) & ~1023u) - smem_u32(smem));
+  StreamShared& sh = *reinterpret_cast<StreamShared*>(rings + R::kBytes);
+  const int w = warp_id(), lane = lane_id(), g = lane >> 2, c = lane & 3;
+  uint8_t* ring = rings + w * R::kStages * R::kStage;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kWarps; ++i)
+      for (int j = 0; j < R::kStages; ++j) mbar_init(&sh.full[i][j], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.rfull[i], kWarps);
+      mbar_init(&sh.rempty[i], 1);
+    }
+    fence_mbar_init();
+  }
+  if (lane == 0 && w < 3) {
+    prefetch_tmap(&maps.w[w]);
+    if (a.Is) prefetch_tmap(&maps.ws[w]);
+  }
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+
+  const int P = a.T * a.k, grid = (int)gridDim.x;
+  const int su = a.Is ? (a.T + kUpTokens - 1) / kUpTokens : 0, sd = a.Is ? (a.T + kDownTokens - 1) / kDownTokens : 0;
+  const int sb = a.Is / 16, ub = a.I / 16, hb = a.H / 16;  // blocks of 16 rows
+  const int us = su * sb;                                  // the shared expert's gate/up units come first
+  const int boxes_h = (a.H + F::kBoxCols - 1) / F::kBoxCols;
+  const int steps_r = ((a.I + F::kBoxCols - 1) / F::kBoxCols + R::kDownBoxes - 1) / R::kDownBoxes;
+  const int steps_s = ((a.Is + F::kBoxCols - 1) / F::kBoxCols + R::kDownBoxes - 1) / R::kDownBoxes;
+  bool dead = false;
+
+  // A warp's walk over its stages: boxes j of gate/up units u = CTA, CTA + grid, ..., then items
+  // i (kDownBoxes boxes) of the down entries x, for row blocks CTA, CTA + grid, ...
+  struct Walk {
+    int n, u, j;       // unit number in the CTA, unit, box
+    int blk, x, i;
+    bool down, end;
+  };
+  int n_up = us, n_mat = 0;  // gate/up units and down entries; without the routed ones before the plan
+  auto share_of = [&](int n) { return (w + kWarps - n % kWarps) % kWarps; };  // rotates: shares differ in boxes
+  auto seek_up = [&](Walk& k) {
+    while (k.u < n_up && k.j >= boxes_h) {
+      ++k.n;
+      k.u += grid;
+      k.j = share_of(k.n);
+    }
+  };
+  auto seek_down = [&](Walk& k) {
+    for (; k.blk < hb; k.blk += grid, k.x = 0, k.i = w) {
+      for (; k.x < n_mat; ++k.x) {
+        const int steps = k.x < n_mat - sd ? steps_r : steps_s;
+        if (k.i < steps) return;
+        k.i -= steps;
+      }
+    }
+    k.end = true;
+  };
+  auto to_down = [&](Walk& k) {
+    k.down = true;
+    k.blk = (int)blockIdx.x, k.x = 0, k.i = w;
+    seek_down(k);
+  };
+  auto next = [&](Walk& k) {
+    if (!k.down) {
+      k.j += kWarps;
+      seek_up(k);
+      if (k.u >= n_up) to_down(k);
+    } else {
+      k.i += kWarps;
+      seek_down(k);
+    }
+  };
+
+  uint32_t issued = 0;
+  Walk head = {0, (int)blockIdx.x, share_of(0), 0, 0, 0, false, false};
+  seek_up(head);
+  // copies of the stage at `head`; the slot is free: its last stage has been read by this warp
+  auto issue = [&] {
+    const int slot = issued % R::kStages;
+    if (lane == 0 && !dead) {
+      uint8_t* stage = ring + slot * R::kStage;
+      uint64_t* bar = &sh.full[w][slot];
+      if (!head.down) {
+        const bool shared = head.u < us;
+        const int v = shared ? head.u : head.u - us;
+        const int row = shared ? v % sb * 16 : (int)entry_e(sh.up[su + v / ub]) * a.I + v % ub * 16;
+        const bool boxed = F::kScaleBoxes && a.boxed[shared ? 2 : 0];
+        mbar_arrive_expect_tx(bar, 2 * (stream::kBoxBytes + (boxed ? F::kScaleBox : 0)));
+        tma_load_2d(stage, shared ? &maps.ws[0] : &maps.w[0], head.j * 128, row, bar);
+        tma_load_2d(stage + stream::kBoxBytes, shared ? &maps.ws[1] : &maps.w[1], head.j * 128, row, bar);
+        if (boxed) {
+          tma_load_2d(stage + 2 * stream::kBoxBytes, shared ? &maps.ss[0] : &maps.s[0], head.j * 8, row, bar);
+          tma_load_2d(stage + 2 * stream::kBoxBytes + F::kScaleBox, shared ? &maps.ss[1] : &maps.s[1], head.j * 8, row, bar);
+        }
+      } else {
+        const uint32_t en = sh.down[head.x];
+        const bool shared = entry_e(en) == kSharedEntry;
+        const int row = (shared ? 0 : (int)entry_e(en) * a.H) + head.blk * 16;
+        const int boxes = ((shared ? a.Is : a.I) + F::kBoxCols - 1) / F::kBoxCols - head.i * R::kDownBoxes;
+        const int n = min(boxes, R::kDownBoxes);
+        const bool boxed = F::kScaleBoxes && a.boxed[shared ? 3 : 1];
+        mbar_arrive_expect_tx(bar, n * (stream::kBoxBytes + (boxed ? F::kScaleBox : 0)));
+        for (int d = 0; d < n; ++d) {
+          const int j = head.i * R::kDownBoxes + d;
+          tma_load_2d(stage + d * stream::kBoxBytes, shared ? &maps.ws[2] : &maps.w[2], j * 128, row, bar);
+          if (boxed)
+            tma_load_2d(stage + 2 * stream::kBoxBytes + d * F::kScaleBox, shared ? &maps.ss[2] : &maps.s[2], j * 8, row, bar);
+        }
+      }
+    }
+    ++issued;
+  };
+  // the shared expert's units need no routing: their copies run while the plan is made
+  while (issued < R::kStages && head.u < us) {
+    issue();
+    head.j += kWarps;
+    seek_up(head);
+  }
+
+  // the plan: routing, the pairs in expert order, entries of up to 8 (gate/up) and 4 (down) tokens
+  for (int t = w; t < a.T; t += kWarps) {
+    const int e = few_topk(a, t);
+    if (lane < a.k) sh.plan.e[t * a.k + lane] = e;
+  }
+  __syncthreads();
+  for (int p = threadIdx.x; p < P; p += kStreamThreads) {
+    const int e = sh.plan.e[p], key = (e < 0 ? 1024 : e) << 9 | p;
+    int rank = 0, place = 0, of = 0;
+    for (int q = 0; q < P; ++q) {
+      const int f = sh.plan.e[q];
+      rank += ((f < 0 ? 1024 : f) << 9 | q) < key;
+      place += f == e && q < p;
+      of += f == e;
+    }
+    sh.pair[rank] = (int16_t)p;
+    sh.plan.by_rank[rank] = e;
+    sh.plan.place[rank] = place << 16 | of;
+  }
+  __syncthreads();
+  if (w == 0) {
+    if (lane < su) sh.up[lane] = pack_entry(kSharedEntry, lane * kUpTokens, min(kUpTokens, a.T - lane * kUpTokens));
+    const int n = list_entries(sh, P, kUpTokens, sh.up, su);
+    if (lane == 0) sh.n_up = n;
+  } else if (w == 1) {
+    const int n = list_entries(sh, P, kDownTokens, sh.down, 0);
+    if (lane < sd) sh.down[n + lane] = pack_entry(kSharedEntry, lane * kDownTokens, min(kDownTokens, a.T - lane * kDownTokens));
+    if (lane == 0) sh.n_down = n + sd;
+  }
+  __syncthreads();
+  n_up = us + (sh.n_up - su) * ub;
+  n_mat = sh.n_down;
+  seek_up(head);
+  if (head.u >= n_up) to_down(head);
+  auto issue_next = [&] {
+    if (head.end) return;
+    issue();
+    next(head);
+  };
+  for (int i = (int)issued; i < R::kStages; ++i) issue_next();
+  for (int t = w; t < a.T; t += kWarps) {  // needed by the down units only
+    const int e = lane < a.k ? sh.plan.e[t * a.k + lane] : -1;
+    const float wt = few_weight(a, t, e);
+    if (lane < a.k) sh.pair_w[t * a.k + lane] = wt;
+    if (blockIdx.x == 0) few_write_route(a, t, e, wt);
+  }
+  __syncthreads();  // the plan's space becomes the units' sums
+
+  const uint16_t* hr = a.h2;                      // h of the routed pairs, [P, I]
+  const uint16_t* hs = a.h2 + (size_t)P * a.I;    // h of the shared expert, [T, Is]
+  uint32_t done = 0;                              // stages read
+  auto landed = [&] {
+    few_wait(&sh.full[w][done % R::kStages], (done / R::kStages) & 1u, dead, a.flags);
+    __syncwarp();
+  };
+  auto read = [&] {
+    __syncwarp();
+    ++done;
+    issue_next();
+  };
+
+  // ---------------------------------------------------------------- gate and up
+  for (int n = 0, u = (int)blockIdx.x; u < n_up; ++n, u += grid) {
+    const bool shared = u < us;
+    const int v = shared ? u : u - us, rows = shared ? sb : ub;
+    const uint32_t en = sh.up[shared ? v / rows : su + v / rows];
+    const int i0 = v % rows * 16, start = entry_start(en), m = entry_n(en);
+    const size_t row = (shared ? 0 : (size_t)entry_e(en) * a.I) + i0 + g;
+    const uint16_t* tok = nullptr;
+    if (g < m) tok = static_cast<const uint16_t*>(a.x) + (size_t)(shared ? start + g : sh.pair[start + g] / a.k) * a.H;
+    const int share = share_of(n);
+    float acc[2][4] = {};
+    uint4 x[F::kLoads], x_next[F::kLoads];
+    auto columns = [&](int j) {
+      stream::load_token<WF>(tok ? tok + j * F::kBoxCols : nullptr, a.H - j * F::kBoxCols, x_next);
+    };
+    if (share < boxes_h) columns(share);
+#pragma unroll 1
+    for (int j = share; j < boxes_h; j += kWarps) {
+#pragma unroll
+      for (int i = 0; i < F::kLoads; ++i) x[i] = x_next[i];
+      if (j + kWarps < boxes_h) columns(j + kWarps);
+      const uint32_t stage = smem_u32(ring + done % R::kStages * R::kStage);
+      stream::Scales sc[2];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        sc[mt].box = stage + 2 * stream::kBoxBytes + mt * F::kScaleBox;
+        sc[mt].in_box = a.boxed[shared ? 2 : 0];
+        sc[mt].left = a.H - j * F::kBoxCols;
+        if constexpr (F::kInt4) {
+          const size_t pitch = (size_t)(a.H >> F::kScaleShift);
+          sc[mt].s0 = (shared ? a.ss[mt] : a.s[mt]) + row * pitch + (j * F::kBoxCols >> F::kScaleShift);
+          sc[mt].s8 = sc[mt].s0 + 8 * pitch;
+        }
+      }
+      landed();
+      stream::mac_box<WF, 2>(stage, x, sc, acc);
+      read();
+    }
+    const int buf = n & 1;
+    few_wait(&sh.rempty[buf], ((n >> 1) & 1) ^ 1, dead, a.flags);
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+      sh.part[buf][share][mt][lane] = make_float4(acc[mt][0], acc[mt][1], acc[mt][2], acc[mt][3]);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.rfull[buf]);
+    if (share != kWarps - 1) continue;
+    // this warp adds up: lane 4g + c holds rows g and g + 8 for tokens 2c and 2c + 1
+    float scale[2][2] = {{1.f, 1.f}, {1.f, 1.f}};
+    if constexpr (WF == MOE_W_INT8_ROW) {
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) scale[mt][r] = __ldg((shared ? a.ss[mt] : a.s[mt]) + row + 8 * r);
+    }
+    few_wait(&sh.rfull[buf], (n >> 1) & 1, dead, a.flags);
+    float sum[2][4] = {};
+#pragma unroll
+    for (int s = 0; s < kWarps; ++s)
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        const float4 p = sh.part[buf][s][mt][lane];
+        sum[mt][0] += p.x, sum[mt][1] += p.y, sum[mt][2] += p.z, sum[mt][3] += p.w;
+      }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.rempty[buf]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int j = 2 * c + (k & 1), r = k >> 1;
+      if (j >= m) continue;
+      const float gate = sum[0][k] * scale[0][r], up = sum[1][k] * scale[1][r];
+      const float h = a.act == MOE_ACT_SILU ? silu_mul(gate, up) : gelu_tanh_mul(gate, up);
+      const uint16_t hi = f32_to_bf16(h);
+      const float rest = h - bf16_to_f32(hi);
+      const size_t at = (shared ? (size_t)P * a.I + (size_t)(start + j) * a.Is : (size_t)sh.pair[start + j] * a.I) + i0 + g + 8 * r;
+      a.h2[at] = hi;
+      a.h2[a.plane + at] = isfinite(rest) ? f32_to_bf16(rest) : (uint16_t)0;
+    }
+  }
+
+  // ---------------------------------------------------------------- every h is stored
+  __syncthreads();
+  for (int i = threadIdx.x; i < kWarps * MOE_FEW_MAX_TOKENS * 16; i += kStreamThreads) (&sh.y[0][0][0])[i] = 0.f;
+  if (threadIdx.x == 0) {
+    __threadfence();
+    atomicAdd(&a.counters[kFewDone], 1u);
+    const uint64_t t0 = global_timer_ns();
+    for (;;) {
+      uint32_t v;
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(&a.counters[kFewDone]) : "memory");
+      if (v >= (uint32_t)grid) break;
+      if (dead || global_timer_ns() - t0 > kWaitLimitNs) {
+        if (!dead) raise_flag(a.flags, MOE_FLAG_TIMEOUT);
+        dead = true;
+        break;
+      }
+    }
+    __threadfence();
+  }
+  __syncthreads();
+
+  // ---------------------------------------------------------------- down and combine
+  struct Item {
+    const uint16_t* tok;
+    uint32_t en;
+    int left, boxes;      // columns and boxes from the item's first box on
+    float s_row;          // int8: scale of the row whose sums the lane will hold
+    const float* s0;      // int4: block scales of row g from the first box on
+    size_t pitch;
+  };
+  constexpr int DB = R::kDownBoxes;
+  uint4 x_next[DB][F::kLoads];
+  auto fetch = [&](const Walk& k) {
+    Item it;
+    it.en = sh.down[k.x];
+    const bool shared = entry_e(it.en) == kSharedEntry;
+    const int K = shared ? a.Is : a.I, j0 = k.i * DB;
+    const size_t row = (shared ? 0 : (size_t)entry_e(it.en) * a.H) + k.blk * 16 + g;
+    it.left = K - j0 * F::kBoxCols;
+    it.boxes = min(DB, (it.left + F::kBoxCols - 1) / F::kBoxCols);
+    it.tok = nullptr;
+    if ((g & 3) < entry_n(it.en)) {
+      const int j = entry_start(it.en) + (g & 3);
+      it.tok = (shared ? hs + (size_t)j * a.Is : hr + (size_t)sh.pair[j] * a.I) + (g < 4 ? 0 : a.plane) + j0 * F::kBoxCols;
+    }
+    it.s_row = 1.f;
+    if constexpr (WF == MOE_W_INT8_ROW) it.s_row = __ldg((shared ? a.ss[2] : a.s[2]) + row + (c < 2 ? 0 : 8));
+    it.pitch = (size_t)(K >> F::kScaleShift);
+    it.s0 = nullptr;
+    if constexpr (F::kInt4) it.s0 = (shared ? a.ss[2] : a.s[2]) + row * it.pitch + (j0 * F::kBoxCols >> F::kScaleShift);
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+      stream::load_token<WF>(it.tok ? it.tok + d * F::kBoxCols : nullptr, it.left - d * F::kBoxCols, x_next[d]);
+    return it;
+  };
+  Walk at = {0, 0, 0, 0, 0, 0, false, false};
+  to_down(at);
+  Item it_next = {};
+  if (!at.end) it_next = fetch(at);
+  for (int blk = (int)blockIdx.x; blk < hb; blk += grid) {
+#pragma unroll 1
+    while (!at.end && at.blk == blk) {
+      const Item it = it_next;
+      uint4 x[DB][F::kLoads];
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < F::kLoads; ++i) x[d][i] = x_next[d][i];
+      next(at);
+      if (!at.end) it_next = fetch(at);
+      const bool shared = entry_e(it.en) == kSharedEntry;
+      const uint32_t stage = smem_u32(ring + done % R::kStages * R::kStage);
+      float acc[1][4] = {};
+      landed();
+#pragma unroll
+      for (int d = 0; d < DB; ++d) {
+        if (d >= it.boxes) break;
+        stream::Scales sc[1];
+        sc[0].box = stage + 2 * stream::kBoxBytes + d * F::kScaleBox;
+        sc[0].in_box = a.boxed[shared ? 3 : 1];
+        sc[0].left = it.left - d * F::kBoxCols;
+        if constexpr (F::kInt4) {
+          sc[0].s0 = it.s0 + (d * F::kBoxCols >> F::kScaleShift);
+          sc[0].s8 = sc[0].s0 + 8 * it.pitch;
+        }
+        stream::mac_box<WF, 1>(stage + d * stream::kBoxBytes, x[d], sc, acc);
+      }
+      read();
+      float v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = acc[0][k] + __shfl_xor_sync(0xFFFFFFFFu, acc[0][k], 2);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int j = 2 * (c & 1) + k;
+        if (j >= entry_n(it.en)) continue;
+        const int p = shared ? 0 : sh.pair[entry_start(it.en) + j];
+        const int to = shared ? entry_start(it.en) + j : p / a.k;
+        const float wt = (shared ? 1.f : sh.pair_w[p]) * it.s_row;
+        sh.y[w][to][c < 2 ? g : g + 8] += wt * (c < 2 ? v[k] : v[2 + k]);
+      }
+      __syncwarp();
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.T * 16; i += kStreamThreads) {
+      const int t = i >> 4, r = i & 15;
+      const size_t to = (size_t)t * a.H + blk * 16 + r;
+      float y = 0.f;
+#pragma unroll
+      for (int s = 0; s < kWarps; ++s) {
+        y += sh.y[s][t][r];
+        sh.y[s][t][r] = 0.f;
+      }
+      if (a.residual) y += bf16_to_f32(static_cast<const uint16_t*>(a.residual)[to]);
+      static_cast<uint16_t*>(a.y)[to] = f32_to_bf16(y);
+    }
+    __syncthreads();
+  }
+  // after a wait that ran out: leave only when the copies have landed
+  if (dead)
+    for (; done < issued; ++done) mbar_wait(&sh.full[w][done % R::kStages], (done / R::kStages) & 1u);
+}
+
 struct FewLayout {
   size_t keys, scores, h, total;
 };
@@ -331,10 +840,51 @@ FewLayout few_layout(const moe_desc& d, int Is, int T) {
 }
 
 template <int WF>
+cudaError_t weight_maps(CUtensorMap* w, CUtensorMap* sc, const void* W, const float* s, uint64_t rows, int K, bool boxed) {
+  using F = stream::Format<WF>;
+  const uint64_t bytes = (uint64_t)K * F::kBits / 8;
+  cudaError_t e = make_tmap(w, W, CU_TENSOR_MAP_DATA_TYPE_UINT8, bytes, rows, bytes, 128, stream::kBoxRows,
+                            CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e == cudaSuccess && boxed)
+    e = make_tmap(sc, s, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, (uint64_t)(K / 32), rows, (uint64_t)(K / 32) * 4, 8,
+                  stream::kBoxRows, CU_TENSOR_MAP_SWIZZLE_NONE);
+  return e;
+}
+
+template <int WF>
+cudaError_t launch_stream(const FewArgs& a, int num_sms, cudaStream_t s) {
+  constexpr size_t smem = 1024 + sizeof(StreamShared) + (size_t)Ring<WF>::kBytes;
+  static_assert(smem <= 232448, "the rings do not fit in shared memory");
+  FewMaps m;
+  cudaError_t e = cudaSuccess;
+  for (int i = 0; i < 3 && e == cudaSuccess; ++i) {
+    const int rows = i < 2 ? a.I : a.H, K = i < 2 ? a.H : a.I;
+    e = weight_maps<WF>(&m.w[i], &m.s[i], a.W[i], a.s[i], (uint64_t)a.E * rows, K, a.boxed[i / 2]);
+    if (e == cudaSuccess && a.Is)
+      e = weight_maps<WF>(&m.ws[i], &m.ss[i], a.Ws[i], a.ss[i], (uint64_t)(i < 2 ? a.Is : a.H), i < 2 ? a.H : a.Is,
+                          a.boxed[2 + i / 2]);
+  }
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(few_stream_kernel<WF>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  // cooperative: the grid's barrier needs every CTA resident (one per SM)
+  return launch_k_cooperative(few_stream_kernel<WF>, dim3(num_sms), dim3(kStreamThreads), smem, s, m, a);
+}
+
+// The scales of a [rows, K] int4 block-32 matrix can be copied by TMA: rows of whole 16-byte
+// pieces, on 16 bytes.
+bool boxed_scales(int wfmt, const float* s, int K) {
+  return wfmt == MOE_W_INT4_B32 && (reinterpret_cast<uintptr_t>(s) % 16) == 0 && K % 128 == 0;
+}
+
+template <int WF>
 cudaError_t launch_layer(const moe_desc& d, const FewArgs& a, int num_sms, cudaStream_t s) {
+  if constexpr (WF != MOE_W_F32)
+    if (d.xfmt == MOE_X_BF16) return launch_stream<WF>(a, num_sms, s);
   const dim3 grid(num_sms * 4), block(kFewThreads);
-  return d.xfmt == MOE_X_F32 ? launch_k(few_layer_kernel<WF, MOE_X_F32>, grid, block, 0, s, a)
-                             : launch_k(few_layer_kernel<WF, MOE_X_BF16>, grid, block, 0, s, a);
+  if (d.xfmt == MOE_X_F32) return launch_k(few_layer_kernel<WF, MOE_X_F32>, grid, block, 0, s, a);
+  if constexpr (WF == MOE_W_F32) return launch_k(few_layer_kernel<WF, MOE_X_BF16>, grid, block, 0, s, a);
+  return cudaErrorInvalidValue;  // not reached
 }
 
 }  // namespace
@@ -348,7 +898,9 @@ cudaError_t launch_few_router(const moe_desc& d, const moe_shared_expert* sh, co
   const FewLayout l = few_layout(d, sh ? sh->I : 0, T);
   char* ws = static_cast<char*>(workspace);
   auto kernel = d.xfmt == MOE_X_F32 ? few_router_kernel<MOE_X_F32> : few_router_kernel<MOE_X_BF16>;
-  return launch_k(kernel, dim3(d.E), dim3(kRouterThreads), 0, s, x, d.W_r, d.b, d.expert_mask, T, d.H, d.E, d.router,
+  int split = kRouterThreads / 32;
+  while (split > 1 && split * T > kRouterThreads / 32) split /= 2;
+  return launch_k(kernel, dim3(d.E), dim3(kRouterThreads), 0, s, x, d.W_r, d.b, d.expert_mask, T, d.H, d.E, d.router, split,
                   reinterpret_cast<uint64_t*>(ws + l.keys), reinterpret_cast<double*>(ws + l.scores),
                   reinterpret_cast<uint32_t*>(ws), flags);
 }
@@ -371,6 +923,14 @@ cudaError_t launch_few_layer(const moe_desc& d, const moe_shared_expert* sh, con
   a.keys = reinterpret_cast<const uint64_t*>(ws + l.keys);
   a.scores = reinterpret_cast<const double*>(ws + l.scores);
   a.h = reinterpret_cast<float*>(ws + l.h);
+  a.h2 = reinterpret_cast<uint16_t*>(ws + l.h);
+  a.plane = (size_t)T * (d.k * (size_t)d.I + a.Is);
+  a.boxed[0] = boxed_scales(d.wfmt, d.s_gate, d.H) && boxed_scales(d.wfmt, d.s_up, d.H);
+  a.boxed[1] = boxed_scales(d.wfmt, d.s_down, d.I);
+  if (sh) {
+    a.boxed[2] = boxed_scales(d.wfmt, sh->s_gate, d.H) && boxed_scales(d.wfmt, sh->s_up, d.H);
+    a.boxed[3] = boxed_scales(d.wfmt, sh->s_down, sh->I);
+  }
   a.counters = reinterpret_cast<uint32_t*>(ws);
   a.idx = idx, a.w = w, a.y = y, a.flags = flags;
   switch (d.wfmt) {

@@ -35,6 +35,25 @@ cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sme
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// Launch of a kernel whose CTAs wait for one another: cooperative, so that it starts only when
+// all of them fit on the GPU beside what already runs.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_k_cooperative(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                                 Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 // Tokens are routed in chunks of this many (token, slot) pairs when building
 // the expert-sorted order.
 constexpr int kPairChunk = 1024;

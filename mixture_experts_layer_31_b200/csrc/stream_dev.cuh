@@ -1,0 +1,190 @@
+// Weight streaming on warp-wide matrix instructions: 16 stored weight rows from shared
+// memory times a few columns (tokens) of bf16.
+//
+// At a few tokens every weight is used once or a few times, so the rate is set by how many
+// weight bytes an SM can take in and by the instructions spent on each.  One m16n8k16
+// instruction multiplies 256 weights with up to 8 tokens, where fp32 lanes would need 8 per
+// token, and takes bf16 weights as they lie in memory: a dot product may visit its terms in
+// any order as long as both operands agree, so a lane reads 16 consecutive bytes of a row
+// and the same columns of the token, and no transposition is needed.  (The tensor cores'
+// tcgen05 form wants 64 rows and 8 tokens at least and its operands in swizzled tiles; with
+// the HBM stream as the bound there is nothing left for it to win here.)
+// Quantised codes are widened exactly:
+//   int8  q = (128 + low 7 bits) - (128 or 256 by the sign bit), both terms exact in bf16
+//   int4  the code (q + 8) goes into the upper mantissa bits of 16: 16 + (q + 8) = q + 24;
+//         an instruction with -24 in every place of the weights takes 24 x out again
+// int8 rows are scaled in the caller's epilogue, int4 blocks here, in fp32.
+#pragma once
+#include "common.cuh"
+
+namespace moe {
+namespace stream {
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) { return __uint_as_float(ld_shared_u32(addr)); }
+
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits) { return (v & mask) | bits; }
+
+// bytes 0 and 2 of w (int8) as a bf16 pair
+__device__ __forceinline__ uint32_t widen_int8(uint32_t w) {
+  uint32_t r;
+  asm("add.rn.bf16x2 %0, %1, %2;"
+      : "=r"(r)
+      : "r"(and_or(w, 0x007F007Fu, 0x43004300u)), "r"(and_or(w, 0x00800080u, 0xC300C300u)));
+  return r;
+}
+
+constexpr uint32_t kMinus24 = 0xC1C0C1C0u;  // bf16 pair of -24
+
+// columns j and j + 4 of the 8 int4 codes in w as a bf16 pair of q + 24
+__device__ __forceinline__ uint32_t widen_int4(uint32_t w, int j) {
+  const uint32_t v = j == 0 ? w << 3 : w >> (4 * j - 3);
+  return (v & 0x00780078u) ^ 0x41C041C0u;
+}
+
+template <int WF>
+struct Format {
+  static constexpr bool kInt4 = WF == MOE_W_INT4_B32 || WF == MOE_W_INT4_B128;
+  static constexpr int kBits = WF == MOE_W_BF16 ? 16 : (WF == MOE_W_INT8_ROW ? 8 : 4);
+  static constexpr int kScaleShift = WF == MOE_W_INT4_B128 ? 7 : 5;  // log2 of the int4 scale block
+  static constexpr int kBoxCols = 128 * 8 / kBits;                   // columns of a box
+  static constexpr int kLoads = kBoxCols / 32;                       // 16-byte token loads of a lane per box
+  // int4 block 32: the 8 scales of a box's 16 rows come as a box of their own (block 128 has
+  // two per row and box, less than TMA copies)
+  static constexpr bool kScaleBoxes = WF == MOE_W_INT4_B32;
+  static constexpr int kScaleBox = kScaleBoxes ? 16 * 32 : 0;
+};
+
+constexpr int kBoxRows = 16;
+constexpr int kBoxBytes = kBoxRows * 128;  // 16 rows x 128 bytes
+
+// Where the int4 block scales of one box's rows are.
+struct Scales {
+  uint32_t box;     // shared address of the scale box, where there is one (in_box)
+  bool in_box;
+  const float* s0;  // else those of the lane's rows g and g + 8, from the box's first column on
+  const float* s8;
+  int left;         // columns of the matrix from the box's first column on
+};
+
+// The columns of the lane's token for one box: 16-byte pieces, zero where there is no token
+// or no column.  `tok` points at the box's first column.
+template <int WF>
+__device__ __forceinline__ void load_token(const uint16_t* tok, int left, uint4 (&x)[Format<WF>::kLoads]) {
+  using F = Format<WF>;
+  const int c = lane_id() & 3;
+#pragma unroll
+  for (int i = 0; i < F::kLoads; ++i) {
+    // int4: word c of unit i; else the lane's 32 bytes of the box, units 2c and 2c + 1
+    const int col = F::kInt4 ? 32 * i + 8 * c : (F::kBoxCols / 4) * c + 8 * i;
+    x[i] = make_uint4(0, 0, 0, 0);
+    if (tok != nullptr && col < left) x[i] = *reinterpret_cast<const uint4*>(tok + col);
+  }
+}
+
+// acc[mt] += box mt (16 rows x 128 bytes at `boxes` + mt kBoxBytes) times the token columns x.
+// The weights lie as TMA puts them: the 16-byte unit u of row r at unit u ^ (r & 7).  Lane
+// 4g + c works on rows g and g + 8.  A quad reads units {0, 2, 4, 6}, then {1, 3, 5, 7} of a row
+// (lane c: 2c and 2c + 1), so that the two rows of an eight-lane phase fall into different
+// banks; int4 lanes read word c of each unit.
+template <int WF, int MT>
+__device__ __forceinline__ void mac_box(uint32_t boxes, const uint4 (&x)[Format<WF>::kLoads], const Scales (&sc)[MT],
+                                        float (&acc)[MT][4]) {
+  using F = Format<WF>;
+  const int g = lane_id() >> 2, c = lane_id() & 3;
+  const uint32_t row = boxes + g * 128;
+  if constexpr (WF == MOE_W_BF16) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t at = row + (((2 * c + h) ^ g) << 4);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const uint4 a = ld_shared_v4(at + mt * kBoxBytes), b = ld_shared_v4(at + mt * kBoxBytes + 1024);
+        mma16816(acc[mt], a.x, b.x, a.y, b.y, x[h].x, x[h].y);
+        mma16816(acc[mt], a.z, b.z, a.w, b.w, x[h].z, x[h].w);
+      }
+    }
+  } else if constexpr (WF == MOE_W_INT8_ROW) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t at = row + (((2 * c + h) ^ g) << 4);
+      uint32_t t[4][2];  // token pairs in the order the widening leaves the codes in: (0, 2), (1, 3)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 v = x[2 * h + (i >> 1)];
+        const uint32_t lo = (i & 1) ? v.z : v.x, hi = (i & 1) ? v.w : v.y;
+        t[i][0] = __byte_perm(lo, hi, 0x5410);
+        t[i][1] = __byte_perm(lo, hi, 0x7632);
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const uint4 av = ld_shared_v4(at + mt * kBoxBytes), bv = ld_shared_v4(at + mt * kBoxBytes + 1024);
+        const uint32_t a[4] = {av.x, av.y, av.z, av.w}, b[4] = {bv.x, bv.y, bv.z, bv.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          mma16816(acc[mt], widen_int8(a[i]), widen_int8(b[i]), widen_int8(a[i] >> 8), widen_int8(b[i] >> 8), t[i][0],
+                   t[i][1]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float s0[MT][4], s8[MT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        if (F::kScaleBoxes && sc[mt].in_box) {
+          const uint32_t at = sc[mt].box + g * 32 + h * 16;
+          const uint4 a = ld_shared_v4(at), b = ld_shared_v4(at + 256);
+          s0[mt][0] = __uint_as_float(a.x), s0[mt][1] = __uint_as_float(a.y);
+          s0[mt][2] = __uint_as_float(a.z), s0[mt][3] = __uint_as_float(a.w);
+          s8[mt][0] = __uint_as_float(b.x), s8[mt][1] = __uint_as_float(b.y);
+          s8[mt][2] = __uint_as_float(b.z), s8[mt][3] = __uint_as_float(b.w);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            // boxes reach past the end of a reduction that is no multiple of theirs: zero weights
+            const int col = 128 * h + 32 * i;
+            const bool in = col < sc[mt].left;
+            s0[mt][i] = in ? __ldg(sc[mt].s0 + (col >> F::kScaleShift)) : 0.f;
+            s8[mt][i] = in ? __ldg(sc[mt].s8 + (col >> F::kScaleShift)) : 0.f;
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 v = x[4 * h + i];
+        const uint32_t b0 = __byte_perm(v.x, v.z, 0x5410), b1 = __byte_perm(v.x, v.z, 0x7632);
+        const uint32_t b2 = __byte_perm(v.y, v.w, 0x5410), b3 = __byte_perm(v.y, v.w, 0x7632);
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        mma16816(d, kMinus24, kMinus24, kMinus24, kMinus24, b0, b1);
+        mma16816(d, kMinus24, kMinus24, kMinus24, kMinus24, b2, b3);
+        const uint32_t at = row + (((4 * h + i) ^ g) << 4) + 4 * c;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const uint32_t a = ld_shared_u32(at + mt * kBoxBytes), b = ld_shared_u32(at + mt * kBoxBytes + 1024);
+          float q[4] = {d[0], d[1], d[2], d[3]};
+          mma16816(q, widen_int4(a, 0), widen_int4(b, 0), widen_int4(a, 1), widen_int4(b, 1), b0, b1);
+          mma16816(q, widen_int4(a, 2), widen_int4(b, 2), widen_int4(a, 3), widen_int4(b, 3), b2, b3);
+          acc[mt][0] = fmaf(q[0], s0[mt][i], acc[mt][0]);
+          acc[mt][1] = fmaf(q[1], s0[mt][i], acc[mt][1]);
+          acc[mt][2] = fmaf(q[2], s8[mt][i], acc[mt][2]);
+          acc[mt][3] = fmaf(q[3], s8[mt][i], acc[mt][3]);
+        }
+      }
+    }
+  }
+}
+
+}  // namespace stream
+}  // namespace moe

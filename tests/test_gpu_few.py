@@ -120,6 +120,19 @@ def test_workload_widths():
     Layer(H=2048, I=768, E=12, k=8, wfmt="int4", router="softmax", scale=1.0).run(3)
 
 
+@pytest.mark.parametrize("wfmt,T,shared", [("bf16", 1, 2048), ("int8", 4, 512), ("int4", 16, 0), ("int4b128", 2, 1024)])
+def test_many_calls_in_a_row_at_workload_widths(wfmt, T, shared):
+    """Rings that go round many times: every call has the first one's bits, and no wait runs
+    out (the fixture looks at the flags)."""
+    layer = Layer(H=2304, I=2048, E=16, k=8, wfmt=wfmt, shared=shared)
+    x = layer.x(T).cuda()
+    first = [t.clone() for t in layer.dev.few(x, residual=x)]
+    for _ in range(30):
+        outs = [layer.dev.few(x, residual=x) for _ in range(5)]
+        assert all(torch.equal(a, b) for o in outs for a, b in zip(o, first))
+        assert moe.moe_device_flags() == 0
+
+
 def test_mask_equals_slice():
     """Masked experts are never chosen; the result has the same bits as the sliced layer's."""
     full = Layer(E=16, k=4, active=[1, 3, 4, 8, 9, 15])
