@@ -403,7 +403,7 @@ struct StreamShared {
   uint64_t rfull[2], rempty[2];  // the warps' sums of a unit written / added up
   int n_up, n_down;              // entries
   float pair_w[kMaxPairs];
-  int16_t pair[kMaxPairs];       // valid pairs in expert order
+  uint16_t pair[kMaxPairs];      // valid pairs in expert order: pair | token << 9
   uint32_t up[kMaxPairs + 2], down[kMaxPairs + 4];  // entries: shared first / shared last
   union {
     float4 part[2][kWarps][2][32];             // [unit parity][share][gate, up]
@@ -470,99 +470,112 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   const int P = a.T * a.k, grid = (int)gridDim.x;
   const int su = a.Is ? (a.T + kUpTokens - 1) / kUpTokens : 0, sd = a.Is ? (a.T + kDownTokens - 1) / kDownTokens : 0;
   const int sb = a.Is / 16, ub = a.I / 16, hb = a.H / 16;  // blocks of 16 rows
-  const int us = su * sb;                                  // the shared expert's gate/up units come first
   const int boxes_h = (a.H + F::kBoxCols - 1) / F::kBoxCols;
-  const int steps_r = ((a.I + F::kBoxCols - 1) / F::kBoxCols + R::kDownBoxes - 1) / R::kDownBoxes;
-  const int steps_s = ((a.Is + F::kBoxCols - 1) / F::kBoxCols + R::kDownBoxes - 1) / R::kDownBoxes;
+  const int boxes_i = (a.I + F::kBoxCols - 1) / F::kBoxCols, boxes_s = (a.Is + F::kBoxCols - 1) / F::kBoxCols;
+  const int steps_r = (boxes_i + R::kDownBoxes - 1) / R::kDownBoxes, steps_s = (boxes_s + R::kDownBoxes - 1) / R::kDownBoxes;
   bool dead = false;
 
-  // A warp's walk over its stages: boxes j of gate/up units u = CTA, CTA + grid, ..., then items
-  // i (kDownBoxes boxes) of the down entries x, for row blocks CTA, CTA + grid, ...
-  struct Walk {
-    int n, u, j;       // unit number in the CTA, unit, box
-    int blk, x, i;
-    bool down, end;
+  // The CTA's gate/up units are numbers CTA, CTA + grid, ... of the entries' blocks of 16 rows.
+  // Their boxes, one unit after the other, go round the warps; so do, for every 16 rows of
+  // y, the down entries' stages.
+  struct UpWalk {
+    int n, entry, block, j;  // the CTA's n-th unit: entry and block of rows; box
   };
-  int n_up = us, n_mat = 0;  // gate/up units and down entries; without the routed ones before the plan
-  auto share_of = [&](int n) { return (w + kWarps - n % kWarps) % kWarps; };  // rotates: shares differ in boxes
-  auto seek_up = [&](Walk& k) {
-    while (k.u < n_up && k.j >= boxes_h) {
-      ++k.n;
-      k.u += grid;
-      k.j = share_of(k.n);
+  struct DownWalk {
+    int blk, x, i;  // block of y's rows, entry, stage
+  };
+  int n_up = su, n_down = 0;  // entries; without the routed ones before the plan
+  auto step_unit = [&](UpWalk& k) {
+    ++k.n;
+    k.block += grid;
+    for (int of; k.block >= (of = k.entry < su ? sb : ub); ++k.entry) k.block -= of;
+  };
+  auto first_unit = [&](int j) {
+    UpWalk k = {-1, 0, (int)blockIdx.x - grid, j};
+    step_unit(k);
+    return k;
+  };
+  auto seek_up = [&](UpWalk& k) {
+    while (k.j >= boxes_h) {
+      k.j -= boxes_h;
+      step_unit(k);
     }
   };
-  auto seek_down = [&](Walk& k) {
-    for (; k.blk < hb; k.blk += grid, k.x = 0, k.i = w) {
-      for (; k.x < n_mat; ++k.x) {
-        const int steps = k.x < n_mat - sd ? steps_r : steps_s;
-        if (k.i < steps) return;
-        k.i -= steps;
+  auto seek_down = [&](DownWalk& k) {
+    for (;;) {
+      if (k.x >= n_down) {
+        k.blk += grid;
+        k.x = 0, k.i = w;
+        if (k.blk >= hb || n_down == 0) return;
       }
+      const int steps = k.x < n_down - sd ? steps_r : steps_s;
+      if (k.i < steps) return;
+      k.i -= steps;
+      ++k.x;
     }
-    k.end = true;
   };
-  auto to_down = [&](Walk& k) {
-    k.down = true;
-    k.blk = (int)blockIdx.x, k.x = 0, k.i = w;
-    seek_down(k);
-  };
-  auto next = [&](Walk& k) {
-    if (!k.down) {
-      k.j += kWarps;
-      seek_up(k);
-      if (k.u >= n_up) to_down(k);
-    } else {
-      k.i += kWarps;
-      seek_down(k);
-    }
+  auto first_down = [&] {
+    DownWalk k = {(int)blockIdx.x, 0, w};
+    if (n_down == 0) k.blk = hb;
+    if (k.blk < hb) seek_down(k);
+    return k;
   };
 
-  uint32_t issued = 0;
-  Walk head = {0, (int)blockIdx.x, share_of(0), 0, 0, 0, false, false};
+  // copies run kStages ahead: `head` and `head_down` are the next to start
+  int issued = 0, in_slot = 0;
+  UpWalk head = first_unit(w);
   seek_up(head);
-  // copies of the stage at `head`; the slot is free: its last stage has been read by this warp
-  auto issue = [&] {
-    const int slot = issued % R::kStages;
+  DownWalk head_down = {hb, 0, 0};
+  auto issue = [&](bool down) {
     if (lane == 0 && !dead) {
-      uint8_t* stage = ring + slot * R::kStage;
-      uint64_t* bar = &sh.full[w][slot];
-      if (!head.down) {
-        const bool shared = head.u < us;
-        const int v = shared ? head.u : head.u - us;
-        const int row = shared ? v % sb * 16 : (int)entry_e(sh.up[su + v / ub]) * a.I + v % ub * 16;
+      uint8_t* stage = ring + in_slot * R::kStage;
+      uint64_t* bar = &sh.full[w][in_slot];
+      if (!down) {
+        const bool shared = head.entry < su;
+        const int row = head.block * 16 + (shared ? 0 : (int)entry_e(sh.up[head.entry]) * a.I);
         const bool boxed = F::kScaleBoxes && a.boxed[shared ? 2 : 0];
+        const CUtensorMap* wm = shared ? maps.ws : maps.w;
         mbar_arrive_expect_tx(bar, 2 * (stream::kBoxBytes + (boxed ? F::kScaleBox : 0)));
-        tma_load_2d(stage, shared ? &maps.ws[0] : &maps.w[0], head.j * 128, row, bar);
-        tma_load_2d(stage + stream::kBoxBytes, shared ? &maps.ws[1] : &maps.w[1], head.j * 128, row, bar);
+        tma_load_2d(stage, wm, head.j * 128, row, bar);
+        tma_load_2d(stage + stream::kBoxBytes, wm + 1, head.j * 128, row, bar);
         if (boxed) {
-          tma_load_2d(stage + 2 * stream::kBoxBytes, shared ? &maps.ss[0] : &maps.s[0], head.j * 8, row, bar);
-          tma_load_2d(stage + 2 * stream::kBoxBytes + F::kScaleBox, shared ? &maps.ss[1] : &maps.s[1], head.j * 8, row, bar);
+          const CUtensorMap* sm = shared ? maps.ss : maps.s;
+          tma_load_2d(stage + 2 * stream::kBoxBytes, sm, head.j * 8, row, bar);
+          tma_load_2d(stage + 2 * stream::kBoxBytes + F::kScaleBox, sm + 1, head.j * 8, row, bar);
         }
       } else {
-        const uint32_t en = sh.down[head.x];
-        const bool shared = entry_e(en) == kSharedEntry;
-        const int row = (shared ? 0 : (int)entry_e(en) * a.H) + head.blk * 16;
-        const int boxes = ((shared ? a.Is : a.I) + F::kBoxCols - 1) / F::kBoxCols - head.i * R::kDownBoxes;
-        const int n = min(boxes, R::kDownBoxes);
+        const uint32_t e = entry_e(sh.down[head_down.x]);
+        const bool shared = e == kSharedEntry;
+        const int row = head_down.blk * 16 + (shared ? 0 : (int)e * a.H);
+        const int j = head_down.i * R::kDownBoxes;
+        const int n = min((shared ? boxes_s : boxes_i) - j, R::kDownBoxes);
         const bool boxed = F::kScaleBoxes && a.boxed[shared ? 3 : 1];
+        const CUtensorMap* wm = shared ? maps.ws + 2 : maps.w + 2;
         mbar_arrive_expect_tx(bar, n * (stream::kBoxBytes + (boxed ? F::kScaleBox : 0)));
-        for (int d = 0; d < n; ++d) {
-          const int j = head.i * R::kDownBoxes + d;
-          tma_load_2d(stage + d * stream::kBoxBytes, shared ? &maps.ws[2] : &maps.w[2], j * 128, row, bar);
-          if (boxed)
-            tma_load_2d(stage + 2 * stream::kBoxBytes + d * F::kScaleBox, shared ? &maps.ss[2] : &maps.s[2], j * 8, row, bar);
-        }
+        tma_load_2d(stage, wm, j * 128, row, bar);
+        if (R::kDownBoxes > 1 && n > 1) tma_load_2d(stage + stream::kBoxBytes, wm, j * 128 + 128, row, bar);
+        if (boxed) tma_load_2d(stage + 2 * stream::kBoxBytes, shared ? maps.ss + 2 : maps.s + 2, j * 8, row, bar);
       }
     }
     ++issued;
+    in_slot = in_slot + 1 == R::kStages ? 0 : in_slot + 1;
   };
-  // the shared expert's units need no routing: their copies run while the plan is made
-  while (issued < R::kStages && head.u < us) {
-    issue();
+  auto issue_up = [&] {
+    issue(false);
     head.j += kWarps;
     seek_up(head);
-  }
+  };
+  auto issue_next = [&] {
+    if (head.entry < n_up) {
+      issue_up();
+    } else if (head_down.blk < hb) {
+      issue(true);
+      head_down.i += kWarps;
+      seek_down(head_down);
+    }
+  };
+  // the shared expert's units need no routing: their copies run while the plan is made
+  while (issued < R::kStages && head.entry < n_up) issue_up();
 
   // the plan: routing, the pairs in expert order, entries of up to 8 (gate/up) and 4 (down) tokens
   for (int t = w; t < a.T; t += kWarps) {
@@ -570,16 +583,26 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     if (lane < a.k) sh.plan.e[t * a.k + lane] = e;
   }
   __syncthreads();
+  const int P4 = (P + 3) & ~3;
+  if (threadIdx.x < P4 - P) sh.plan.e[P + threadIdx.x] = -1;  // past every pair
+  __syncthreads();
   for (int p = threadIdx.x; p < P; p += kStreamThreads) {
-    const int e = sh.plan.e[p], key = (e < 0 ? 1024 : e) << 9 | p;
-    int rank = 0, place = 0, of = 0;
-    for (int q = 0; q < P; ++q) {
-      const int f = sh.plan.e[q];
-      rank += ((f < 0 ? 1024 : f) << 9 | q) < key;
-      place += f == e && q < p;
-      of += f == e;
+    const int e = sh.plan.e[p], mine = e < 0 ? 1024 : e;
+    int before = 0, place = 0, of = 0;
+#pragma unroll 2
+    for (int q = 0; q < P4; q += 4) {
+      const int4 f = *reinterpret_cast<const int4*>(&sh.plan.e[q]);
+      const int v[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        before += (uint32_t)v[i] < (uint32_t)mine;  // -1 lies past every expert
+        const bool same = v[i] == e;
+        of += same;
+        place += same && q + i < p;
+      }
     }
-    sh.pair[rank] = (int16_t)p;
+    const int rank = before + place;
+    sh.pair[rank] = (uint16_t)(p | (p / a.k) << 9);
     sh.plan.by_rank[rank] = e;
     sh.plan.place[rank] = place << 16 | of;
   }
@@ -594,68 +617,130 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     if (lane == 0) sh.n_down = n + sd;
   }
   __syncthreads();
-  n_up = us + (sh.n_up - su) * ub;
-  n_mat = sh.n_down;
-  seek_up(head);
-  if (head.u >= n_up) to_down(head);
-  auto issue_next = [&] {
-    if (head.end) return;
-    issue();
-    next(head);
-  };
-  for (int i = (int)issued; i < R::kStages; ++i) issue_next();
-  for (int t = w; t < a.T; t += kWarps) {  // needed by the down units only
-    const int e = lane < a.k ? sh.plan.e[t * a.k + lane] : -1;
-    const float wt = few_weight(a, t, e);
-    if (lane < a.k) sh.pair_w[t * a.k + lane] = wt;
-    if (blockIdx.x == 0) few_write_route(a, t, e, wt);
-  }
-  __syncthreads();  // the plan's space becomes the units' sums
+  n_up = sh.n_up;
+  n_down = sh.n_down;
+  head_down = first_down();
+  for (int i = issued; i < R::kStages; ++i) issue_next();
+  // this warp's tokens' experts, for the weights later; then the plan's space becomes the units' sums
+  int my_e[2] = {-1, -1};
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (w + i * kWarps < a.T && lane < a.k) my_e[i] = sh.plan.e[(w + i * kWarps) * a.k + lane];
+  static_assert(MOE_FEW_MAX_TOKENS <= 2 * kWarps, "a warp has at most two tokens' weights");
+  __syncthreads();
 
   const uint16_t* hr = a.h2;                      // h of the routed pairs, [P, I]
   const uint16_t* hs = a.h2 + (size_t)P * a.I;    // h of the shared expert, [T, Is]
-  uint32_t done = 0;                              // stages read
+  int done = 0, out_slot = 0;                     // stages read
+  uint32_t phase = 0;
   auto landed = [&] {
-    few_wait(&sh.full[w][done % R::kStages], (done / R::kStages) & 1u, dead, a.flags);
+    few_wait(&sh.full[w][out_slot], phase, dead, a.flags);
     __syncwarp();
   };
   auto read = [&] {
     __syncwarp();
     ++done;
+    if (++out_slot == R::kStages) out_slot = 0, phase ^= 1u;
     issue_next();
   };
 
   // ---------------------------------------------------------------- gate and up
-  for (int n = 0, u = (int)blockIdx.x; u < n_up; ++n, u += grid) {
-    const bool shared = u < us;
-    const int v = shared ? u : u - us, rows = shared ? sb : ub;
-    const uint32_t en = sh.up[shared ? v / rows : su + v / rows];
-    const int i0 = v % rows * 16, start = entry_start(en), m = entry_n(en);
-    const size_t row = (shared ? 0 : (size_t)entry_e(en) * a.I) + i0 + g;
-    const uint16_t* tok = nullptr;
-    if (g < m) tok = static_cast<const uint16_t*>(a.x) + (size_t)(shared ? start + g : sh.pair[start + g] / a.k) * a.H;
-    const int share = share_of(n);
+  {
     float acc[2][4] = {};
-    uint4 x[F::kLoads], x_next[F::kLoads];
-    auto columns = [&](int j) {
-      stream::load_token<WF>(tok ? tok + j * F::kBoxCols : nullptr, a.H - j * F::kBoxCols, x_next);
+    UpWalk unit = first_unit(0);  // the next to hand over
+    // this warp's sums of the unit to shared memory; the warp whose turn it is adds them up
+    auto hand_over = [&] {
+      const int buf = unit.n & 1, parity = (unit.n >> 1) & 1;
+      const int from = unit.n * boxes_h % kWarps, shares = min(boxes_h, kWarps);  // the warps that had boxes
+      few_wait(&sh.rempty[buf], parity ^ 1, dead, a.flags);
+      if ((w + kWarps - from) % kWarps < shares) {
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          sh.part[buf][w][mt][lane] = make_float4(acc[mt][0], acc[mt][1], acc[mt][2], acc[mt][3]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[mt][k] = 0.f;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.rfull[buf]);
+      if (unit.n % kWarps == w) {
+        const bool shared = unit.entry < su;
+        const uint32_t en = sh.up[unit.entry];
+        const int i0 = unit.block * 16 + g, start = entry_start(en), m = entry_n(en);
+        // lane 4g + c holds rows g and g + 8 for tokens 2c and 2c + 1
+        float scale[2][2] = {{1.f, 1.f}, {1.f, 1.f}};
+        if constexpr (WF == MOE_W_INT8_ROW) {
+          const size_t row = (shared ? 0 : (size_t)entry_e(en) * a.I) + i0;
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) scale[mt][r] = __ldg((shared ? a.ss[mt] : a.s[mt]) + row + 8 * r);
+        }
+        size_t to[2];  // where the two tokens' h go
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int j = min(2 * c + i, m - 1);
+          to[i] = (shared ? (size_t)P * a.I + (size_t)(start + j) * a.Is : (size_t)(sh.pair[start + j] & 511) * a.I) + i0;
+        }
+        few_wait(&sh.rfull[buf], parity, dead, a.flags);
+        float sum[2][4] = {};
+        int s = from;
+#pragma unroll 4
+        for (int i = 0; i < shares; ++i, s = s + 1 == kWarps ? 0 : s + 1) {
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
+            const float4 p = sh.part[buf][s][mt][lane];
+            sum[mt][0] += p.x, sum[mt][1] += p.y, sum[mt][2] += p.z, sum[mt][3] += p.w;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.rempty[buf]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (2 * c + (k & 1) >= m) continue;
+          const float gate = sum[0][k] * scale[0][k >> 1], up = sum[1][k] * scale[1][k >> 1];
+          const float h = a.act == MOE_ACT_SILU ? silu_mul(gate, up) : gelu_tanh_mul(gate, up);
+          const uint16_t hi = f32_to_bf16(h);
+          const float rest = h - bf16_to_f32(hi);
+          uint16_t* at = a.h2 + to[k & 1] + 8 * (k >> 1);
+          at[0] = hi;
+          at[a.plane] = isfinite(rest) ? f32_to_bf16(rest) : (uint16_t)0;
+        }
+      }
+      step_unit(unit);
     };
-    if (share < boxes_h) columns(share);
+    UpWalk at = first_unit(w);
+    seek_up(at);
+    uint4 x[F::kLoads], x_next[F::kLoads];
+    auto fetch = [&] {
+      const uint32_t en = sh.up[at.entry];
+      const int j = entry_start(en) + min(g, entry_n(en) - 1);  // columns past the tokens are not used
+      const int t = at.entry < su ? j : sh.pair[j] >> 9;
+      stream::load_token<WF>(static_cast<const uint16_t*>(a.x) + (size_t)t * a.H + at.j * F::kBoxCols,
+                             a.H - at.j * F::kBoxCols, x_next);
+    };
+    if (at.entry < n_up) fetch();
 #pragma unroll 1
-    for (int j = share; j < boxes_h; j += kWarps) {
+    while (at.entry < n_up) {
+      while (unit.n < at.n) hand_over();
+      const UpWalk k = at;
 #pragma unroll
       for (int i = 0; i < F::kLoads; ++i) x[i] = x_next[i];
-      if (j + kWarps < boxes_h) columns(j + kWarps);
-      const uint32_t stage = smem_u32(ring + done % R::kStages * R::kStage);
+      at.j += kWarps;
+      seek_up(at);
+      if (at.entry < n_up) fetch();
+      const uint32_t stage = smem_u32(ring + out_slot * R::kStage);
       stream::Scales sc[2];
+      if constexpr (F::kInt4) {
+        const bool shared = k.entry < su;
+        const size_t row = (shared ? 0 : (size_t)entry_e(sh.up[k.entry]) * a.I) + k.block * 16 + g;
+        const size_t pitch = (size_t)(a.H >> F::kScaleShift);
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        sc[mt].box = stage + 2 * stream::kBoxBytes + mt * F::kScaleBox;
-        sc[mt].in_box = a.boxed[shared ? 2 : 0];
-        sc[mt].left = a.H - j * F::kBoxCols;
-        if constexpr (F::kInt4) {
-          const size_t pitch = (size_t)(a.H >> F::kScaleShift);
-          sc[mt].s0 = (shared ? a.ss[mt] : a.s[mt]) + row * pitch + (j * F::kBoxCols >> F::kScaleShift);
+        for (int mt = 0; mt < 2; ++mt) {
+          sc[mt].box = stage + 2 * stream::kBoxBytes + mt * F::kScaleBox;
+          sc[mt].in_box = a.boxed[shared ? 2 : 0];
+          sc[mt].left = a.H - k.j * F::kBoxCols;
+          sc[mt].s0 = (shared ? a.ss[mt] : a.s[mt]) + row * pitch + (k.j * F::kBoxCols >> F::kScaleShift);
           sc[mt].s8 = sc[mt].s0 + 8 * pitch;
         }
       }
@@ -663,45 +748,16 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       stream::mac_box<WF, 2>(stage, x, sc, acc);
       read();
     }
-    const int buf = n & 1;
-    few_wait(&sh.rempty[buf], ((n >> 1) & 1) ^ 1, dead, a.flags);
+    while (unit.entry < n_up) hand_over();
+  }
+  // the weights, while the grid finishes; the down units need them
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
-      sh.part[buf][share][mt][lane] = make_float4(acc[mt][0], acc[mt][1], acc[mt][2], acc[mt][3]);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.rfull[buf]);
-    if (share != kWarps - 1) continue;
-    // this warp adds up: lane 4g + c holds rows g and g + 8 for tokens 2c and 2c + 1
-    float scale[2][2] = {{1.f, 1.f}, {1.f, 1.f}};
-    if constexpr (WF == MOE_W_INT8_ROW) {
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) scale[mt][r] = __ldg((shared ? a.ss[mt] : a.s[mt]) + row + 8 * r);
-    }
-    few_wait(&sh.rfull[buf], (n >> 1) & 1, dead, a.flags);
-    float sum[2][4] = {};
-#pragma unroll
-    for (int s = 0; s < kWarps; ++s)
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        const float4 p = sh.part[buf][s][mt][lane];
-        sum[mt][0] += p.x, sum[mt][1] += p.y, sum[mt][2] += p.z, sum[mt][3] += p.w;
-      }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.rempty[buf]);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int j = 2 * c + (k & 1), r = k >> 1;
-      if (j >= m) continue;
-      const float gate = sum[0][k] * scale[0][r], up = sum[1][k] * scale[1][r];
-      const float h = a.act == MOE_ACT_SILU ? silu_mul(gate, up) : gelu_tanh_mul(gate, up);
-      const uint16_t hi = f32_to_bf16(h);
-      const float rest = h - bf16_to_f32(hi);
-      const size_t at = (shared ? (size_t)P * a.I + (size_t)(start + j) * a.Is : (size_t)sh.pair[start + j] * a.I) + i0 + g + 8 * r;
-      a.h2[at] = hi;
-      a.h2[a.plane + at] = isfinite(rest) ? f32_to_bf16(rest) : (uint16_t)0;
-    }
+  for (int i = 0; i < 2; ++i) {
+    const int t = w + i * kWarps;
+    if (t >= a.T) break;
+    const float wt = few_weight(a, t, my_e[i]);
+    if (lane < a.k) sh.pair_w[t * a.k + lane] = wt;
+    if (blockIdx.x == 0) few_write_route(a, t, my_e[i], wt);
   }
 
   // ---------------------------------------------------------------- every h is stored
@@ -727,65 +783,60 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 
   // ---------------------------------------------------------------- down and combine
   struct Item {
-    const uint16_t* tok;
     uint32_t en;
-    int left, boxes;      // columns and boxes from the item's first box on
+    int left;             // columns from the item's first box on
     float s_row;          // int8: scale of the row whose sums the lane will hold
     const float* s0;      // int4: block scales of row g from the first box on
     size_t pitch;
   };
   constexpr int DB = R::kDownBoxes;
   uint4 x_next[DB][F::kLoads];
-  auto fetch = [&](const Walk& k) {
+  auto fetch = [&](const DownWalk& k) {
     Item it;
     it.en = sh.down[k.x];
     const bool shared = entry_e(it.en) == kSharedEntry;
-    const int K = shared ? a.Is : a.I, j0 = k.i * DB;
+    const int K = shared ? a.Is : a.I, c0 = k.i * DB * F::kBoxCols;
     const size_t row = (shared ? 0 : (size_t)entry_e(it.en) * a.H) + k.blk * 16 + g;
-    it.left = K - j0 * F::kBoxCols;
-    it.boxes = min(DB, (it.left + F::kBoxCols - 1) / F::kBoxCols);
-    it.tok = nullptr;
-    if ((g & 3) < entry_n(it.en)) {
-      const int j = entry_start(it.en) + (g & 3);
-      it.tok = (shared ? hs + (size_t)j * a.Is : hr + (size_t)sh.pair[j] * a.I) + (g < 4 ? 0 : a.plane) + j0 * F::kBoxCols;
-    }
+    it.left = K - c0;
+    const int j = entry_start(it.en) + min(g & 3, entry_n(it.en) - 1);  // columns past the tokens are not used
+    const uint16_t* tok = (shared ? hs + (size_t)j * a.Is : hr + (size_t)(sh.pair[j] & 511) * a.I) + (g < 4 ? 0 : a.plane) + c0;
     it.s_row = 1.f;
     if constexpr (WF == MOE_W_INT8_ROW) it.s_row = __ldg((shared ? a.ss[2] : a.s[2]) + row + (c < 2 ? 0 : 8));
     it.pitch = (size_t)(K >> F::kScaleShift);
     it.s0 = nullptr;
-    if constexpr (F::kInt4) it.s0 = (shared ? a.ss[2] : a.s[2]) + row * it.pitch + (j0 * F::kBoxCols >> F::kScaleShift);
+    if constexpr (F::kInt4) it.s0 = (shared ? a.ss[2] : a.s[2]) + row * it.pitch + (c0 >> F::kScaleShift);
 #pragma unroll
     for (int d = 0; d < DB; ++d)
-      stream::load_token<WF>(it.tok ? it.tok + d * F::kBoxCols : nullptr, it.left - d * F::kBoxCols, x_next[d]);
+      if (d == 0 || it.left > d * F::kBoxCols) stream::load_token<WF>(tok + d * F::kBoxCols, it.left - d * F::kBoxCols, x_next[d]);
     return it;
   };
-  Walk at = {0, 0, 0, 0, 0, 0, false, false};
-  to_down(at);
+  DownWalk at = first_down();
   Item it_next = {};
-  if (!at.end) it_next = fetch(at);
+  if (at.blk < hb) it_next = fetch(at);
   for (int blk = (int)blockIdx.x; blk < hb; blk += grid) {
 #pragma unroll 1
-    while (!at.end && at.blk == blk) {
+    while (at.blk == blk) {
       const Item it = it_next;
       uint4 x[DB][F::kLoads];
 #pragma unroll
       for (int d = 0; d < DB; ++d)
 #pragma unroll
         for (int i = 0; i < F::kLoads; ++i) x[d][i] = x_next[d][i];
-      next(at);
-      if (!at.end) it_next = fetch(at);
+      at.i += kWarps;
+      seek_down(at);
+      if (at.blk < hb) it_next = fetch(at);
       const bool shared = entry_e(it.en) == kSharedEntry;
-      const uint32_t stage = smem_u32(ring + done % R::kStages * R::kStage);
+      const uint32_t stage = smem_u32(ring + out_slot * R::kStage);
       float acc[1][4] = {};
       landed();
 #pragma unroll
       for (int d = 0; d < DB; ++d) {
-        if (d >= it.boxes) break;
+        if (d > 0 && it.left <= d * F::kBoxCols) break;
         stream::Scales sc[1];
-        sc[0].box = stage + 2 * stream::kBoxBytes + d * F::kScaleBox;
-        sc[0].in_box = a.boxed[shared ? 3 : 1];
-        sc[0].left = it.left - d * F::kBoxCols;
         if constexpr (F::kInt4) {
+          sc[0].box = stage + 2 * stream::kBoxBytes + d * F::kScaleBox;
+          sc[0].in_box = a.boxed[shared ? 3 : 1];
+          sc[0].left = it.left - d * F::kBoxCols;
           sc[0].s0 = it.s0 + (d * F::kBoxCols >> F::kScaleShift);
           sc[0].s8 = sc[0].s0 + 8 * it.pitch;
         }
@@ -799,9 +850,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       for (int k = 0; k < 2; ++k) {
         const int j = 2 * (c & 1) + k;
         if (j >= entry_n(it.en)) continue;
-        const int p = shared ? 0 : sh.pair[entry_start(it.en) + j];
-        const int to = shared ? entry_start(it.en) + j : p / a.k;
-        const float wt = (shared ? 1.f : sh.pair_w[p]) * it.s_row;
+        const int p = sh.pair[shared ? 0 : entry_start(it.en) + j];
+        const int to = shared ? entry_start(it.en) + j : p >> 9;
+        const float wt = (shared ? 1.f : sh.pair_w[p & 511]) * it.s_row;
         sh.y[w][to][c < 2 ? g : g + 8] += wt * (c < 2 ? v[k] : v[2 + k]);
       }
       __syncwarp();
@@ -822,8 +873,12 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     __syncthreads();
   }
   // after a wait that ran out: leave only when the copies have landed
-  if (dead)
-    for (; done < issued; ++done) mbar_wait(&sh.full[w][done % R::kStages], (done / R::kStages) & 1u);
+  if (dead) {
+    for (; done < issued; ++done) {
+      mbar_wait(&sh.full[w][out_slot], phase);
+      if (++out_slot == R::kStages) out_slot = 0, phase ^= 1u;
+    }
+  }
 }
 
 struct FewLayout {

@@ -78,18 +78,25 @@ struct Scales {
   int left;         // columns of the matrix from the box's first column on
 };
 
-// The columns of the lane's token for one box: 16-byte pieces, zero where there is no token
-// or no column.  `tok` points at the box's first column.
+// The columns of the lane's token for one box; `tok` points at the box's first column, `left`
+// columns follow there.  Past the end of a reduction that is no multiple of a box the
+// weights read as zero, and so must the token.
 template <int WF>
 __device__ __forceinline__ void load_token(const uint16_t* tok, int left, uint4 (&x)[Format<WF>::kLoads]) {
   using F = Format<WF>;
   const int c = lane_id() & 3;
+  // int4: word c of each unit; else the lane's 32 bytes of the box, units 2c and 2c + 1
+  const int first = F::kInt4 ? 8 * c : (F::kBoxCols / 4) * c;
+  constexpr int kNext = F::kInt4 ? 32 : 8;
+  if (left >= F::kBoxCols) {
 #pragma unroll
-  for (int i = 0; i < F::kLoads; ++i) {
-    // int4: word c of unit i; else the lane's 32 bytes of the box, units 2c and 2c + 1
-    const int col = F::kInt4 ? 32 * i + 8 * c : (F::kBoxCols / 4) * c + 8 * i;
-    x[i] = make_uint4(0, 0, 0, 0);
-    if (tok != nullptr && col < left) x[i] = *reinterpret_cast<const uint4*>(tok + col);
+    for (int i = 0; i < F::kLoads; ++i) x[i] = *reinterpret_cast<const uint4*>(tok + first + kNext * i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < F::kLoads; ++i) {
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (first + kNext * i < left) x[i] = *reinterpret_cast<const uint4*>(tok + first + kNext * i);
+    }
   }
 }
 
