@@ -14,7 +14,7 @@
 // are running and do not wait themselves: the wait ends however many CTAs are resident and
 // whatever else runs on the GPU.  It is bounded in time all the same (MOE_FLAG_TIMEOUT).
 // The router launch zeroes the counters, so the workspace needs no initial state.
-#include <type_traits>
+#include <algorithm>
 
 #include "common.cuh"
 #include "internal.h"
@@ -44,61 +44,85 @@ __device__ __forceinline__ void load4(const void* base, size_t i, float (&v)[4])
   }
 }
 
-// One CTA per expert.  Its warps share out the tokens, or, where there are fewer tokens than
-// warps, `split` warps share a token's columns; a lane keeps four 16-byte loads of the
-// router row in flight.
-template <int XF>
+// One CTA per kRouterExperts experts.  Its warps share out the columns; each keeps the sums of
+// all tokens (in passes of TT) so that a router weight is widened to 64 bits once for all of
+// them: the conversions, not the 64-bit multiply-adds, are what this costs (a token for each
+// warp instead took 20 us at 16 tokens x 2,304 columns x 256 experts).
+constexpr int kRouterExperts = 2;
+
+template <int XF, int TT>
 __global__ void __launch_bounds__(kRouterThreads)
     few_router_kernel(const void* __restrict__ x, const float* __restrict__ W_r, const float* __restrict__ bias,
-                      const uint8_t* __restrict__ mask, int T, int H, int E, int router, int split,
-                      uint64_t* __restrict__ keys, double* __restrict__ scores, uint32_t* __restrict__ counters,
-                      uint32_t* flags) {
+                      const uint8_t* __restrict__ mask, int T, int H, int E, int router, uint64_t* __restrict__ keys,
+                      double* __restrict__ scores, uint32_t* __restrict__ counters, uint32_t* flags) {
   pdl_wait();
   pdl_trigger();
-  __shared__ double part[MOE_FEW_MAX_TOKENS][kRouterThreads / 32];
-  const int e = blockIdx.x, tid = threadIdx.x, w = warp_id(), lane = lane_id();
-  if (e == 0 && tid < kFewCounters) counters[tid] = 0;
-  const float* row = W_r + (size_t)e * H;
-  const int share = w % split, step = split * 128;
-  for (int t = w / split; t < T; t += (kRouterThreads / 32) / split) {
-    double acc[4] = {0.0, 0.0, 0.0, 0.0};
-    for (int c0 = share * 128 + lane * 4; c0 < H; c0 += 4 * step) {
-      float r[4][4], v[4][4];
+  constexpr int kSums = kRouterExperts * TT, kRWarps = kRouterThreads / 32;
+  __shared__ double part[kRWarps][kSums];
+  const int e0 = blockIdx.x * kRouterExperts, tid = threadIdx.x, w = warp_id(), lane = lane_id();
+  if (blockIdx.x == 0 && tid < kFewCounters) counters[tid] = 0;
+  const float* row[kRouterExperts];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int c = c0 + j * step;
+  for (int i = 0; i < kRouterExperts; ++i) row[i] = W_r + (size_t)min(e0 + i, E - 1) * H;
+  for (int t0 = 0; t0 < T; t0 += TT) {
+    double acc[kSums] = {};
+#pragma unroll 2
+    for (int c = w * 128 + lane * 4; c < H; c += kRWarps * 128) {
+      float v[kRouterExperts][4], u[TT][4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) r[j][q] = v[j][q] = 0.f;
-        if (c < H) {
-          load4<MOE_X_F32>(row, c, r[j]);
-          load4<XF>(x, (size_t)t * H + c, v[j]);
+      for (int i = 0; i < kRouterExperts; ++i) load4<MOE_X_F32>(row[i], c, v[i]);
+#pragma unroll
+      for (int j = 0; j < TT; ++j) load4<XF>(x, (size_t)min(t0 + j, T - 1) * H + c, u[j]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        double wd[kRouterExperts];
+#pragma unroll
+        for (int i = 0; i < kRouterExperts; ++i) wd[i] = (double)v[i][q];
+#pragma unroll
+        for (int j = 0; j < TT; ++j) {
+          const double xd = (double)u[j][q];
+#pragma unroll
+          for (int i = 0; i < kRouterExperts; ++i) acc[j * kRouterExperts + i] = fma(wd[i], xd, acc[j * kRouterExperts + i]);
         }
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[q] = fma((double)r[j][q], (double)v[j][q], acc[q]);
     }
-    double l = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+    // sums over the lanes: halves of the values change sides until each lane has at most one
+    int n = kSums, first = 0;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, off);
-    if (lane == 0) part[t][share] = l;
-  }
-  __syncthreads();
-  if (tid < T) {
-    const int t = tid;
-    double l = 0.0;
-    for (int s = 0; s < split; ++s) l += part[t][s];
-    const bool finite = isfinite((float)l);
-    if (!finite) raise_flag(flags, MOE_FLAG_NONFINITE_LOGIT);
-    double score = l, key = l;
-    if (router == MOE_ROUTER_SIGMOID_BIAS) {
-      score = 1.0 / (1.0 + exp(-l));
-      key = score + (bias ? (double)bias[e] : 0.0);
+    for (int off = 16; off > 0; off >>= 1) {
+      if (n > 1) {
+        n >>= 1;
+        const bool up = (lane & off) != 0;
+#pragma unroll
+        for (int k = 0; k < kSums / 2; ++k) {
+          if (k >= n) break;
+          const double give = up ? acc[k] : acc[k + n], keep = up ? acc[k + n] : acc[k];
+          acc[k] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, off);
+        }
+        if (up) first += n;
+      } else {
+        acc[0] += __shfl_xor_sync(0xFFFFFFFFu, acc[0], off);
+      }
     }
-    const bool open = finite && key == key && (mask == nullptr || mask[e] != 0);
-    keys[(size_t)t * E + e] = open ? sortable(key) : 0;
-    scores[(size_t)t * E + e] = score;
+    part[w][first] = acc[0];  // lanes with the same value write the same sum
+    __syncthreads();
+    const int j = tid / kRouterExperts, e = e0 + tid % kRouterExperts, t = t0 + j;
+    if (tid < kSums && t < T && e < E) {
+      double l = 0.0;
+#pragma unroll
+      for (int i = 0; i < kRWarps; ++i) l += part[i][tid];
+      const bool finite = isfinite((float)l);
+      if (!finite) raise_flag(flags, MOE_FLAG_NONFINITE_LOGIT);
+      double score = l, key = l;
+      if (router == MOE_ROUTER_SIGMOID_BIAS) {
+        score = 1.0 / (1.0 + exp(-l));
+        key = score + (bias ? (double)bias[e] : 0.0);
+      }
+      const bool open = finite && key == key && (mask == nullptr || mask[e] != 0);
+      keys[(size_t)t * E + e] = open ? sortable(key) : 0;
+      scores[(size_t)t * E + e] = score;
+    }
+    __syncthreads();
   }
 }
 
@@ -120,6 +144,7 @@ struct FewArgs {
   // int4 block scales come with the weights as boxes, per matrix, or are read where they
   // lie: [0] routed gate/up, [1] routed down, [2], [3] shared
   uint8_t boxed[4];
+  int team, down_team;  // warps that share a gate/up unit, a down entry
   uint32_t* counters; // [0] claimed units, [kFewDone] finished gate/up units
   int32_t* idx;
   float* w;
@@ -400,13 +425,13 @@ __device__ __forceinline__ int entry_n(uint32_t v) { return (int)(v >> 21); }
 
 struct StreamShared {
   uint64_t full[kWarps][kMaxStages];
-  uint64_t rfull[2], rempty[2];  // the warps' sums of a unit written / added up
+  uint64_t rfull[kWarps][2], rempty[kWarps][2];  // by team: its warps' sums of a unit written / added up
   int n_up, n_down;              // entries
   float pair_w[kMaxPairs];
   uint16_t pair[kMaxPairs];      // valid pairs in expert order: pair | token << 9
   uint32_t up[kMaxPairs + 2], down[kMaxPairs + 4];  // entries: shared first / shared last
   union {
-    float4 part[2][kWarps][2][32];             // [unit parity][share][gate, up]
+    float4 part[2][kWarps][2][32];             // [unit parity][warp][gate, up]
     float y[kWarps][MOE_FEW_MAX_TOKENS][16];   // down: each warp's share of 16 rows
     struct {
       int e[kMaxPairs];                        // building the plan: by pair
@@ -453,10 +478,11 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kWarps; ++i)
       for (int j = 0; j < R::kStages; ++j) mbar_init(&sh.full[i][j], 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.rfull[i], kWarps);
-      mbar_init(&sh.rempty[i], 1);
-    }
+    for (int i = 0; i < kWarps / a.team; ++i)
+      for (int j = 0; j < 2; ++j) {
+        mbar_init(&sh.rfull[i][j], a.team);
+        mbar_init(&sh.rempty[i][j], 1);
+      }
     fence_mbar_init();
   }
   if (lane == 0 && w < 3) {
@@ -475,11 +501,13 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   const int steps_r = (boxes_i + R::kDownBoxes - 1) / R::kDownBoxes, steps_s = (boxes_s + R::kDownBoxes - 1) / R::kDownBoxes;
   bool dead = false;
 
-  // The CTA's gate/up units are numbers CTA, CTA + grid, ... of the entries' blocks of 16 rows.
-  // Their boxes, one unit after the other, go round the warps; so do, for every 16 rows of
-  // y, the down entries' stages.
+  // Teams of warps take the units in turn: numbers team, team + teams, ... of the entries'
+  // blocks of 16 rows (of the down entries, for every 16 rows of y).  Within a team the
+  // boxes, one unit after the other, go round the warps.
+  const int up_teams = kWarps / a.team, up_team = w / a.team, up_w = w % a.team;
+  const int down_teams = kWarps / a.down_team, down_team = w / a.down_team, down_w = w % a.down_team;
   struct UpWalk {
-    int n, entry, block, j;  // the CTA's n-th unit: entry and block of rows; box
+    int n, entry, block, j;  // the team's n-th unit: entry and block of rows; box
   };
   struct DownWalk {
     int blk, x, i;  // block of y's rows, entry, stage
@@ -487,11 +515,11 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   int n_up = su, n_down = 0;  // entries; without the routed ones before the plan
   auto step_unit = [&](UpWalk& k) {
     ++k.n;
-    k.block += grid;
+    k.block += grid * up_teams;
     for (int of; k.block >= (of = k.entry < su ? sb : ub); ++k.entry) k.block -= of;
   };
   auto first_unit = [&](int j) {
-    UpWalk k = {-1, 0, (int)blockIdx.x - grid, j};
+    UpWalk k = {-1, 0, ((int)blockIdx.x - grid) * up_teams + up_team, j};
     step_unit(k);
     return k;
   };
@@ -505,25 +533,27 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     for (;;) {
       if (k.x >= n_down) {
         k.blk += grid;
-        k.x = 0, k.i = w;
-        if (k.blk >= hb || n_down == 0) return;
+        k.x = down_team, k.i = down_w;
+        if (k.blk >= hb || k.x >= n_down) {
+          k.blk = hb;
+          return;
+        }
       }
       const int steps = k.x < n_down - sd ? steps_r : steps_s;
       if (k.i < steps) return;
       k.i -= steps;
-      ++k.x;
+      k.x += down_teams;
     }
   };
   auto first_down = [&] {
-    DownWalk k = {(int)blockIdx.x, 0, w};
-    if (n_down == 0) k.blk = hb;
-    if (k.blk < hb) seek_down(k);
+    DownWalk k = {(int)blockIdx.x - grid, n_down, 0};
+    seek_down(k);
     return k;
   };
 
   // copies run kStages ahead: `head` and `head_down` are the next to start
   int issued = 0, in_slot = 0;
-  UpWalk head = first_unit(w);
+  UpWalk head = first_unit(up_w);
   seek_up(head);
   DownWalk head_down = {hb, 0, 0};
   auto issue = [&](bool down) {
@@ -562,7 +592,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   };
   auto issue_up = [&] {
     issue(false);
-    head.j += kWarps;
+    head.j += a.team;
     seek_up(head);
   };
   auto issue_next = [&] {
@@ -570,7 +600,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       issue_up();
     } else if (head_down.blk < hb) {
       issue(true);
-      head_down.i += kWarps;
+      head_down.i += a.down_team;
       seek_down(head_down);
     }
   };
@@ -651,9 +681,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     // this warp's sums of the unit to shared memory; the warp whose turn it is adds them up
     auto hand_over = [&] {
       const int buf = unit.n & 1, parity = (unit.n >> 1) & 1;
-      const int from = unit.n * boxes_h % kWarps, shares = min(boxes_h, kWarps);  // the warps that had boxes
-      few_wait(&sh.rempty[buf], parity ^ 1, dead, a.flags);
-      if ((w + kWarps - from) % kWarps < shares) {
+      const int from = a.team == 1 ? 0 : unit.n * boxes_h % a.team;  // the warps that had boxes, in their order
+      const int shares = min(boxes_h, a.team);
+      few_wait(&sh.rempty[up_team][buf], parity ^ 1, dead, a.flags);
+      if (shares == a.team || (up_w >= from ? up_w - from : up_w + a.team - from) < shares) {
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
           sh.part[buf][w][mt][lane] = make_float4(acc[mt][0], acc[mt][1], acc[mt][2], acc[mt][3]);
@@ -662,8 +693,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.rfull[buf]);
-      if (unit.n % kWarps == w) {
+      if (lane == 0) mbar_arrive(&sh.rfull[up_team][buf]);
+      if (a.team == 1 || unit.n % a.team == up_w) {
         const bool shared = unit.entry < su;
         const uint32_t en = sh.up[unit.entry];
         const int i0 = unit.block * 16 + g, start = entry_start(en), m = entry_n(en);
@@ -682,19 +713,19 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           const int j = min(2 * c + i, m - 1);
           to[i] = (shared ? (size_t)P * a.I + (size_t)(start + j) * a.Is : (size_t)(sh.pair[start + j] & 511) * a.I) + i0;
         }
-        few_wait(&sh.rfull[buf], parity, dead, a.flags);
+        few_wait(&sh.rfull[up_team][buf], parity, dead, a.flags);
         float sum[2][4] = {};
         int s = from;
 #pragma unroll 4
-        for (int i = 0; i < shares; ++i, s = s + 1 == kWarps ? 0 : s + 1) {
+        for (int i = 0; i < shares; ++i, s = s + 1 == a.team ? 0 : s + 1) {
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt) {
-            const float4 p = sh.part[buf][s][mt][lane];
+            const float4 p = sh.part[buf][up_team * a.team + s][mt][lane];
             sum[mt][0] += p.x, sum[mt][1] += p.y, sum[mt][2] += p.z, sum[mt][3] += p.w;
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.rempty[buf]);
+        if (lane == 0) mbar_arrive(&sh.rempty[up_team][buf]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           if (2 * c + (k & 1) >= m) continue;
@@ -709,41 +740,48 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       }
       step_unit(unit);
     };
-    UpWalk at = first_unit(w);
+    UpWalk at = first_unit(up_w);
     seek_up(at);
     uint4 x[F::kLoads], x_next[F::kLoads];
-    auto fetch = [&] {
+    const uint16_t* tok = nullptr;  // the lane's token, of the unit at `at`
+    size_t row = 0;                 // int4: row of the block scales
+    auto unit_of = [&] {
       const uint32_t en = sh.up[at.entry];
       const int j = entry_start(en) + min(g, entry_n(en) - 1);  // columns past the tokens are not used
       const int t = at.entry < su ? j : sh.pair[j] >> 9;
-      stream::load_token<WF>(static_cast<const uint16_t*>(a.x) + (size_t)t * a.H + at.j * F::kBoxCols,
-                             a.H - at.j * F::kBoxCols, x_next);
+      tok = static_cast<const uint16_t*>(a.x) + (size_t)t * a.H;
+      if constexpr (F::kInt4) row = (at.entry < su ? 0 : (size_t)entry_e(en) * a.I) + at.block * 16 + g;
     };
-    if (at.entry < n_up) fetch();
+    auto fetch = [&] { stream::load_token<WF>(tok + at.j * F::kBoxCols, a.H - at.j * F::kBoxCols, x_next); };
+    if (at.entry < n_up) {
+      unit_of();
+      fetch();
+    }
 #pragma unroll 1
     while (at.entry < n_up) {
       while (unit.n < at.n) hand_over();
-      const UpWalk k = at;
 #pragma unroll
       for (int i = 0; i < F::kLoads; ++i) x[i] = x_next[i];
-      at.j += kWarps;
-      seek_up(at);
-      if (at.entry < n_up) fetch();
       const uint32_t stage = smem_u32(ring + out_slot * R::kStage);
       stream::Scales sc[2];
       if constexpr (F::kInt4) {
-        const bool shared = k.entry < su;
-        const size_t row = (shared ? 0 : (size_t)entry_e(sh.up[k.entry]) * a.I) + k.block * 16 + g;
+        const bool shared = at.entry < su;
         const size_t pitch = (size_t)(a.H >> F::kScaleShift);
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
           sc[mt].box = stage + 2 * stream::kBoxBytes + mt * F::kScaleBox;
           sc[mt].in_box = a.boxed[shared ? 2 : 0];
-          sc[mt].left = a.H - k.j * F::kBoxCols;
-          sc[mt].s0 = (shared ? a.ss[mt] : a.s[mt]) + row * pitch + (k.j * F::kBoxCols >> F::kScaleShift);
+          sc[mt].left = a.H - at.j * F::kBoxCols;
+          sc[mt].s0 = (shared ? a.ss[mt] : a.s[mt]) + row * pitch + (at.j * F::kBoxCols >> F::kScaleShift);
           sc[mt].s8 = sc[mt].s0 + 8 * pitch;
         }
       }
+      at.j += a.team;
+      if (at.j >= boxes_h) {
+        seek_up(at);
+        if (at.entry < n_up) unit_of();
+      }
+      if (at.entry < n_up) fetch();
       landed();
       stream::mac_box<WF, 2>(stage, x, sc, acc);
       read();
@@ -782,77 +820,92 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   __syncthreads();
 
   // ---------------------------------------------------------------- down and combine
-  struct Item {
-    uint32_t en;
-    int left;             // columns from the item's first box on
-    float s_row;          // int8: scale of the row whose sums the lane will hold
-    const float* s0;      // int4: block scales of row g from the first box on
-    size_t pitch;
-  };
   constexpr int DB = R::kDownBoxes;
   uint4 x_next[DB][F::kLoads];
-  auto fetch = [&](const DownWalk& k) {
-    Item it;
-    it.en = sh.down[k.x];
-    const bool shared = entry_e(it.en) == kSharedEntry;
-    const int K = shared ? a.Is : a.I, c0 = k.i * DB * F::kBoxCols;
-    const size_t row = (shared ? 0 : (size_t)entry_e(it.en) * a.H) + k.blk * 16 + g;
-    it.left = K - c0;
-    const int j = entry_start(it.en) + min(g & 3, entry_n(it.en) - 1);  // columns past the tokens are not used
-    const uint16_t* tok = (shared ? hs + (size_t)j * a.Is : hr + (size_t)(sh.pair[j] & 511) * a.I) + (g < 4 ? 0 : a.plane) + c0;
-    it.s_row = 1.f;
-    if constexpr (WF == MOE_W_INT8_ROW) it.s_row = __ldg((shared ? a.ss[2] : a.s[2]) + row + (c < 2 ? 0 : 8));
-    it.pitch = (size_t)(K >> F::kScaleShift);
-    it.s0 = nullptr;
-    if constexpr (F::kInt4) it.s0 = (shared ? a.ss[2] : a.s[2]) + row * it.pitch + (c0 >> F::kScaleShift);
+  DownWalk at = first_down();
+  // of the entry at `at`: its tokens, reduction length, the lane's token (value or remainder)
+  uint32_t en = 0;
+  int K = 0;
+  const uint16_t* tok = nullptr;
+  float s_row = 1.f;      // int8: scale of the row whose sums the lane will hold
+  const float* s0 = nullptr;  // int4: block scales of row g
+  auto entry_of = [&] {
+    en = sh.down[at.x];
+    const bool shared = entry_e(en) == kSharedEntry;
+    const size_t row = (shared ? 0 : (size_t)entry_e(en) * a.H) + at.blk * 16 + g;
+    const int j = entry_start(en) + min(g & 3, entry_n(en) - 1);  // columns past the tokens are not used
+    K = shared ? a.Is : a.I;
+    tok = (shared ? hs + (size_t)j * a.Is : hr + (size_t)(sh.pair[j] & 511) * a.I) + (g < 4 ? 0 : a.plane);
+    if constexpr (WF == MOE_W_INT8_ROW) s_row = __ldg((shared ? a.ss[2] : a.s[2]) + row + (c < 2 ? 0 : 8));
+    if constexpr (F::kInt4) s0 = (shared ? a.ss[2] : a.s[2]) + row * (size_t)(K >> F::kScaleShift);
+  };
+  auto fetch = [&] {
+    const int c0 = at.i * DB * F::kBoxCols, left = K - c0;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
-      if (d == 0 || it.left > d * F::kBoxCols) stream::load_token<WF>(tok + d * F::kBoxCols, it.left - d * F::kBoxCols, x_next[d]);
-    return it;
+      if (d == 0 || left > d * F::kBoxCols)
+        stream::load_token<WF>(tok + c0 + d * F::kBoxCols, left - d * F::kBoxCols, x_next[d]);
   };
-  DownWalk at = first_down();
-  Item it_next = {};
-  if (at.blk < hb) it_next = fetch(at);
+  if (at.blk < hb) {
+    entry_of();
+    fetch();
+  }
   for (int blk = (int)blockIdx.x; blk < hb; blk += grid) {
+    float acc[1][4] = {};
 #pragma unroll 1
     while (at.blk == blk) {
-      const Item it = it_next;
       uint4 x[DB][F::kLoads];
 #pragma unroll
       for (int d = 0; d < DB; ++d)
 #pragma unroll
         for (int i = 0; i < F::kLoads; ++i) x[d][i] = x_next[d][i];
-      at.i += kWarps;
-      seek_down(at);
-      if (at.blk < hb) it_next = fetch(at);
-      const bool shared = entry_e(it.en) == kSharedEntry;
       const uint32_t stage = smem_u32(ring + out_slot * R::kStage);
-      float acc[1][4] = {};
+      const int c0 = at.i * DB * F::kBoxCols, left = K - c0;
+      stream::Scales sc[DB][1];
+      if constexpr (F::kInt4) {
+#pragma unroll
+        for (int d = 0; d < DB; ++d) {
+          sc[d][0].box = stage + 2 * stream::kBoxBytes + d * F::kScaleBox;
+          sc[d][0].in_box = a.boxed[entry_e(en) == kSharedEntry ? 3 : 1];
+          sc[d][0].left = left - d * F::kBoxCols;
+          sc[d][0].s0 = s0 + (c0 + d * F::kBoxCols >> F::kScaleShift);
+          sc[d][0].s8 = sc[d][0].s0 + 8 * (size_t)(K >> F::kScaleShift);
+        }
+      }
+      // the next stage's tokens, of the same entry or of the next
+      const uint32_t now = en;
+      const float s_now = s_row;
+      const int x_now = at.x;
+      at.i += a.down_team;
+      seek_down(at);
+      const bool last = at.x != x_now || at.blk != blk;
+      if (at.blk < hb) {
+        if (last) entry_of();
+        fetch();
+      }
       landed();
 #pragma unroll
       for (int d = 0; d < DB; ++d) {
-        if (d > 0 && it.left <= d * F::kBoxCols) break;
-        stream::Scales sc[1];
-        if constexpr (F::kInt4) {
-          sc[0].box = stage + 2 * stream::kBoxBytes + d * F::kScaleBox;
-          sc[0].in_box = a.boxed[shared ? 3 : 1];
-          sc[0].left = it.left - d * F::kBoxCols;
-          sc[0].s0 = it.s0 + (d * F::kBoxCols >> F::kScaleShift);
-          sc[0].s8 = sc[0].s0 + 8 * it.pitch;
-        }
-        stream::mac_box<WF, 1>(stage + d * stream::kBoxBytes, x[d], sc, acc);
+        if (d > 0 && left <= d * F::kBoxCols) break;
+        stream::mac_box<WF, 1>(stage + d * stream::kBoxBytes, x[d], sc[d], acc);
       }
       read();
+      if (!last) continue;
+      // the entry's sums, weighted, to this warp's share of y
+      const bool shared = entry_e(now) == kSharedEntry;
       float v[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = acc[0][k] + __shfl_xor_sync(0xFFFFFFFFu, acc[0][k], 2);
+      for (int k = 0; k < 4; ++k) {
+        v[k] = acc[0][k] + __shfl_xor_sync(0xFFFFFFFFu, acc[0][k], 2);
+        acc[0][k] = 0.f;
+      }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int j = 2 * (c & 1) + k;
-        if (j >= entry_n(it.en)) continue;
-        const int p = sh.pair[shared ? 0 : entry_start(it.en) + j];
-        const int to = shared ? entry_start(it.en) + j : p >> 9;
-        const float wt = (shared ? 1.f : sh.pair_w[p & 511]) * it.s_row;
+        if (j >= entry_n(now)) continue;
+        const int p = sh.pair[shared ? 0 : entry_start(now) + j];
+        const int to = shared ? entry_start(now) + j : p >> 9;
+        const float wt = (shared ? 1.f : sh.pair_w[p & 511]) * s_now;
         sh.y[w][to][c < 2 ? g : g + 8] += wt * (c < 2 ? v[k] : v[2 + k]);
       }
       __syncwarp();
@@ -907,9 +960,17 @@ cudaError_t weight_maps(CUtensorMap* w, CUtensorMap* sc, const void* W, const fl
 }
 
 template <int WF>
-cudaError_t launch_stream(const FewArgs& a, int num_sms, cudaStream_t s) {
+cudaError_t launch_stream(FewArgs a, int num_sms, cudaStream_t s) {
   constexpr size_t smem = 1024 + sizeof(StreamShared) + (size_t)Ring<WF>::kBytes;
   static_assert(smem <= 232448, "the rings do not fit in shared memory");
+  // Sharing a unit out costs each warp some hundred instructions of hand-over, which counts where
+  // the widening of the codes bounds the stream; where the units are few, smaller teams leave
+  // warps without work in the last round.  Measured (teams of 12, 3, 1): 1 token bf16 58, 59,
+  // 60 us and int4 28, 30, 46 us; 4 tokens int8 160, 147, 163 us; 16 tokens int8 390, 325,
+  // 328 us.  The tokens' experts are not known here: expect them to differ.
+  const int touched = std::min(a.T * a.k, a.E);
+  a.team = (int64_t)touched * (a.I / 16) >= 4LL * 4 * num_sms ? 3 : kWarps;
+  a.down_team = touched >= 2 * kWarps ? 3 : kWarps;
   FewMaps m;
   cudaError_t e = cudaSuccess;
   for (int i = 0; i < 3 && e == cudaSuccess; ++i) {
@@ -952,12 +1013,14 @@ cudaError_t launch_few_router(const moe_desc& d, const moe_shared_expert* sh, co
                               uint32_t* flags, cudaStream_t s) {
   const FewLayout l = few_layout(d, sh ? sh->I : 0, T);
   char* ws = static_cast<char*>(workspace);
-  auto kernel = d.xfmt == MOE_X_F32 ? few_router_kernel<MOE_X_F32> : few_router_kernel<MOE_X_BF16>;
-  int split = kRouterThreads / 32;
-  while (split > 1 && split * T > kRouterThreads / 32) split /= 2;
-  return launch_k(kernel, dim3(d.E), dim3(kRouterThreads), 0, s, x, d.W_r, d.b, d.expert_mask, T, d.H, d.E, d.router, split,
-                  reinterpret_cast<uint64_t*>(ws + l.keys), reinterpret_cast<double*>(ws + l.scores),
-                  reinterpret_cast<uint32_t*>(ws), flags);
+  auto go = [&](auto kernel) {
+    return launch_k(kernel, dim3((d.E + kRouterExperts - 1) / kRouterExperts), dim3(kRouterThreads), 0, s, x, d.W_r, d.b,
+                    d.expert_mask, T, d.H, d.E, d.router, reinterpret_cast<uint64_t*>(ws + l.keys),
+                    reinterpret_cast<double*>(ws + l.scores), reinterpret_cast<uint32_t*>(ws), flags);
+  };
+  if (d.xfmt == MOE_X_F32)
+    return T == 1 ? go(few_router_kernel<MOE_X_F32, 1>) : (T <= 4 ? go(few_router_kernel<MOE_X_F32, 4>) : go(few_router_kernel<MOE_X_F32, 8>));
+  return T == 1 ? go(few_router_kernel<MOE_X_BF16, 1>) : (T <= 4 ? go(few_router_kernel<MOE_X_BF16, 4>) : go(few_router_kernel<MOE_X_BF16, 8>));
 }
 
 cudaError_t launch_few_layer(const moe_desc& d, const moe_shared_expert* sh, const void* x, int T, int32_t* idx,

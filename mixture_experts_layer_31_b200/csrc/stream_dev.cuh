@@ -27,6 +27,14 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// d = a b + c, with c kept
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1, const float (&c)[4]) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+
 __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
@@ -34,7 +42,17 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
 }
 __device__ __forceinline__ float ld_shared_f32(uint32_t addr) { return __uint_as_float(ld_shared_u32(addr)); }
 
-__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits) { return (v & mask) | bits; }
+// one three-input logic instruction each: (v & mask) | bits, (v & mask) ^ bits
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "r"(mask), "r"(bits));
+  return r;
+}
+__device__ __forceinline__ uint32_t and_xor(uint32_t v, uint32_t mask, uint32_t bits) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(r) : "r"(v), "r"(mask), "r"(bits));
+  return r;
+}
 
 // bytes 0 and 2 of w (int8) as a bf16 pair
 __device__ __forceinline__ uint32_t widen_int8(uint32_t w) {
@@ -50,7 +68,7 @@ constexpr uint32_t kMinus24 = 0xC1C0C1C0u;  // bf16 pair of -24
 // columns j and j + 4 of the 8 int4 codes in w as a bf16 pair of q + 24
 __device__ __forceinline__ uint32_t widen_int4(uint32_t w, int j) {
   const uint32_t v = j == 0 ? w << 3 : w >> (4 * j - 3);
-  return (v & 0x00780078u) ^ 0x41C041C0u;
+  return and_xor(v, 0x00780078u, 0x41C041C0u);
 }
 
 template <int WF>
@@ -180,8 +198,8 @@ __device__ __forceinline__ void mac_box(uint32_t boxes, const uint4 (&x)[Format<
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           const uint32_t a = ld_shared_u32(at + mt * kBoxBytes), b = ld_shared_u32(at + mt * kBoxBytes + 1024);
-          float q[4] = {d[0], d[1], d[2], d[3]};
-          mma16816(q, widen_int4(a, 0), widen_int4(b, 0), widen_int4(a, 1), widen_int4(b, 1), b0, b1);
+          float q[4];
+          mma16816(q, widen_int4(a, 0), widen_int4(b, 0), widen_int4(a, 1), widen_int4(b, 1), b0, b1, d);
           mma16816(q, widen_int4(a, 2), widen_int4(b, 2), widen_int4(a, 3), widen_int4(b, 3), b2, b3);
           acc[mt][0] = fmaf(q[0], s0[mt][i], acc[mt][0]);
           acc[mt][1] = fmaf(q[1], s0[mt][i], acc[mt][1]);
