@@ -204,8 +204,6 @@ cudaError_t launch_few_layer(const moe_desc& d, const moe_shared_expert* sh, con
                              cudaStream_t s);
 // ---- the dense product ----
 size_t linear_workspace_bytes(const moe_linear_desc& d, int M);
-cudaError_t launch_linear_simt(const moe_linear_desc& d, const void* x, int64_t ldx, int M, const void* residual,
-                               int64_t ldr, void* y, int64_t ldy, cudaStream_t s);
 cudaError_t launch_dense_plan(int T, int chunk, int32_t* counts, int32_t* offsets, int32_t* touched,
                               int32_t* group_base, int32_t* tile_base, int32_t* meta, int32_t* sorted_pair,
                               float* ones, cudaStream_t s);

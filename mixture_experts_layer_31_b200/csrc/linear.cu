@@ -6,32 +6,13 @@
 // memory as fp32 (weights decoded on the way in), 4 x 4 sums per thread.
 #include "common.cuh"
 #include "internal.h"
+#include "linear.h"
 
 namespace moe {
 namespace {
 
 constexpr int kTile = 64;
 constexpr int kSlice = 16;
-
-struct LinearArgs {
-  int M, N, K;
-  int act;
-  const void* x;
-  long long ldx;
-  const void* W[2];  // W, W_up
-  const float* s[2];
-  const float* b[2];
-  const void* residual;
-  long long ldr;
-  void* y;
-  long long ldy;
-};
-
-__device__ __forceinline__ float activate(float v, int act) {
-  if (act == MOE_ACT_SILU) return silu_mul(v, 1.f);
-  if (act == MOE_ACT_GELU_TANH) return gelu_tanh_mul(v, 1.f);
-  return v;
-}
 
 // four stored weights of row r from column c on (c a multiple of 4)
 template <int WF>
@@ -56,7 +37,7 @@ __device__ __forceinline__ void weights4(const void* W, const float* s, size_t r
   }
 }
 
-template <int WF, int XF, int YF, bool GATED>
+template <int WF, int XF, bool GATED>
 __global__ void __launch_bounds__(256) linear_simt_kernel(const LinearArgs a) {
   pdl_wait();
   pdl_trigger();
@@ -115,54 +96,24 @@ __global__ void __launch_bounds__(256) linear_simt_kernel(const LinearArgs a) {
     for (int i = 0; i < 4; ++i) {
       const int m = m0 + tm + i;
       if (m >= a.M) break;
-      float v[G];
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        v[g] = acc[g][i][j];
-        if constexpr (WF == MOE_W_INT8_ROW) v[g] *= a.s[g][n];
-        if (a.b[g]) v[g] += a.b[g][n];
-      }
-      float y = activate(v[0], a.act);
-      if constexpr (GATED) y *= v[G - 1];
-      if constexpr (YF == MOE_X_F32) {
-        if (a.residual) y += static_cast<const float*>(a.residual)[(size_t)m * a.ldr + n];
-        static_cast<float*>(a.y)[(size_t)m * a.ldy + n] = y;
-      } else {
-        if (a.residual) y += bf16_to_f32(static_cast<const uint16_t*>(a.residual)[(size_t)m * a.ldr + n]);
-        static_cast<uint16_t*>(a.y)[(size_t)m * a.ldy + n] = f32_to_bf16(y);
-      }
+      linear_finish(a, WF == MOE_W_INT8_ROW, m, n, acc[0][i][j], acc[G - 1][i][j]);
     }
   }
 }
 
-template <int WF, int XF, int YF>
-cudaError_t launch_simt(const LinearArgs& a, cudaStream_t s) {
-  const dim3 grid((a.N + kTile - 1) / kTile, (a.M + kTile - 1) / kTile), block(256);
-  return a.W[1] ? launch_k(linear_simt_kernel<WF, XF, YF, true>, grid, block, 0, s, a)
-                : launch_k(linear_simt_kernel<WF, XF, YF, false>, grid, block, 0, s, a);
-}
-
 template <int WF>
 cudaError_t launch_simt(const moe_linear_desc& d, const LinearArgs& a, cudaStream_t s) {
+  const dim3 grid((a.N + kTile - 1) / kTile, (a.M + kTile - 1) / kTile), block(256);
   if (d.xfmt == MOE_X_F32)
-    return d.yfmt == MOE_X_F32 ? launch_simt<WF, MOE_X_F32, MOE_X_F32>(a, s) : launch_simt<WF, MOE_X_F32, MOE_X_BF16>(a, s);
-  return d.yfmt == MOE_X_F32 ? launch_simt<WF, MOE_X_BF16, MOE_X_F32>(a, s) : launch_simt<WF, MOE_X_BF16, MOE_X_BF16>(a, s);
+    return a.W[1] ? launch_k(linear_simt_kernel<WF, MOE_X_F32, true>, grid, block, 0, s, a)
+                  : launch_k(linear_simt_kernel<WF, MOE_X_F32, false>, grid, block, 0, s, a);
+  return a.W[1] ? launch_k(linear_simt_kernel<WF, MOE_X_BF16, true>, grid, block, 0, s, a)
+                : launch_k(linear_simt_kernel<WF, MOE_X_BF16, false>, grid, block, 0, s, a);
 }
 
 }  // namespace
 
-size_t linear_workspace_bytes(const moe_linear_desc& d, int M) {
-  (void)d;
-  (void)M;
-  return 0;
-}
-
-cudaError_t launch_linear_simt(const moe_linear_desc& d, const void* x, int64_t ldx, int M, const void* residual,
-                               int64_t ldr, void* y, int64_t ldy, cudaStream_t s) {
-  LinearArgs a = {};
-  a.M = M, a.N = d.N, a.K = d.K, a.act = d.act;
-  a.x = x, a.ldx = ldx, a.residual = residual, a.ldr = ldr, a.y = y, a.ldy = ldy;
-  a.W[0] = d.W, a.W[1] = d.W_up, a.s[0] = d.s, a.s[1] = d.s_up, a.b[0] = d.b, a.b[1] = d.b_up;
+cudaError_t launch_linear_simt(const moe_linear_desc& d, const LinearArgs& a, cudaStream_t s) {
   switch (d.wfmt) {
     case MOE_W_F32: return launch_simt<MOE_W_F32>(d, a, s);
     case MOE_W_BF16: return launch_simt<MOE_W_BF16>(d, a, s);

@@ -1,0 +1,54 @@
+// Shared by the kernels of the dense product (moe_linear).
+#pragma once
+#include "common.cuh"
+
+namespace moe {
+
+struct LinearArgs {
+  int M, N, K;
+  int act, yfmt;
+  const void* x;
+  long long ldx;
+  const void* W[2];  // W, W_up (NULL: not gated)
+  const float* s[2];
+  const float* b[2];
+  const void* residual;
+  long long ldr;
+  void* y;
+  long long ldy;
+};
+
+// up to this many tokens the weights stream through warp-wide matrix instructions
+constexpr int kLinearStreamTokens = 64;
+
+__device__ __forceinline__ float linear_act(float v, int act) {
+  if (act == MOE_ACT_SILU) return silu_mul(v, 1.f);
+  if (act == MOE_ACT_GELU_TANH) return gelu_tanh_mul(v, 1.f);
+  return v;
+}
+
+// y[m, n] from the sums of W (v) and W_up (u): row scales of int8 weights, bias, activation,
+// gate, residual, one rounding.  The residual's element is read before y's is written.
+__device__ __forceinline__ void linear_finish(const LinearArgs& a, bool row_scales, int m, int n, float v, float u) {
+  if (row_scales) v *= __ldg(a.s[0] + n);
+  if (a.b[0]) v += __ldg(a.b[0] + n);
+  float y = linear_act(v, a.act);
+  if (a.W[1]) {
+    if (row_scales) u *= __ldg(a.s[1] + n);
+    if (a.b[1]) u += __ldg(a.b[1] + n);
+    y *= u;
+  }
+  if (a.yfmt == MOE_X_F32) {
+    if (a.residual) y += static_cast<const float*>(a.residual)[(size_t)m * a.ldr + n];
+    static_cast<float*>(a.y)[(size_t)m * a.ldy + n] = y;
+  } else {
+    if (a.residual) y += bf16_to_f32(static_cast<const uint16_t*>(a.residual)[(size_t)m * a.ldr + n]);
+    static_cast<uint16_t*>(a.y)[(size_t)m * a.ldy + n] = f32_to_bf16(y);
+  }
+}
+
+bool linear_stream_ok(const moe_linear_desc& d, int M);
+cudaError_t launch_linear_stream(const moe_linear_desc& d, const LinearArgs& a, int num_sms, uint32_t* flags, cudaStream_t s);
+cudaError_t launch_linear_simt(const moe_linear_desc& d, const LinearArgs& a, cudaStream_t s);
+
+}  // namespace moe

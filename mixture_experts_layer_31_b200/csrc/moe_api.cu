@@ -19,6 +19,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "linear.h"
 #include "moe.h"
 
 namespace moe {
@@ -668,6 +669,12 @@ static moe_status validate_linear(const moe_linear_desc* d, int32_t M) {
   return MOE_OK;
 }
 
+size_t moe::linear_workspace_bytes(const moe_linear_desc& d, int M) {
+  (void)d;
+  (void)M;
+  return 0;
+}
+
 extern "C" moe_status moe_linear_workspace_size(const moe_linear_desc* d, int32_t M, size_t* bytes) {
   g_err.clear();
   moe_status st = validate_linear(d, M);
@@ -698,7 +705,15 @@ extern "C" moe_status moe_linear(const moe_linear_desc* d, const void* x, int64_
   if ((st = check_scratch(workspace, ws_bytes, linear_workspace_bytes(*d, M))) != MOE_OK) return st;
   DeviceState* dev = nullptr;
   if ((st = device_state(&dev)) != MOE_OK) return st;
-  MOE_LAUNCH("linear_simt", stream, launch_linear_simt(*d, x, ldx, M, residual, ldr, y, ldy, stream));
+  LinearArgs a = {};
+  a.M = M, a.N = d->N, a.K = d->K, a.act = d->act, a.yfmt = d->yfmt;
+  a.x = x, a.ldx = ldx, a.residual = residual, a.ldr = ldr, a.y = y, a.ldy = ldy;
+  a.W[0] = d->W, a.W[1] = d->W_up, a.s[0] = d->s, a.s[1] = d->s_up, a.b[0] = d->b, a.b[1] = d->b_up;
+  if (linear_stream_ok(*d, M)) {
+    MOE_LAUNCH("linear_stream", stream, launch_linear_stream(*d, a, dev->num_sms, dev->flags, stream));
+    return MOE_OK;
+  }
+  MOE_LAUNCH("linear_simt", stream, launch_linear_simt(*d, a, stream));
   return MOE_OK;
 }
 

@@ -96,6 +96,27 @@ struct Scales {
   int left;         // columns of the matrix from the box's first column on
 };
 
+// int4 block scales of the lane's rows g and g + 8 for the four units of half h of a box
+template <int WF>
+__device__ __forceinline__ void load_block_scales(const Scales& sc, int h, float (&s0)[4], float (&s8)[4]) {
+  using F = Format<WF>;
+  if (F::kScaleBoxes && sc.in_box) {
+    const uint32_t at = sc.box + (lane_id() >> 2) * 32 + h * 16;
+    const uint4 a = ld_shared_v4(at), b = ld_shared_v4(at + 256);
+    s0[0] = __uint_as_float(a.x), s0[1] = __uint_as_float(a.y), s0[2] = __uint_as_float(a.z), s0[3] = __uint_as_float(a.w);
+    s8[0] = __uint_as_float(b.x), s8[1] = __uint_as_float(b.y), s8[2] = __uint_as_float(b.z), s8[3] = __uint_as_float(b.w);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // boxes reach past the end of a reduction that is no multiple of theirs: zero weights
+      const int col = 128 * h + 32 * i;
+      const bool in = col < sc.left;
+      s0[i] = in ? __ldg(sc.s0 + (col >> F::kScaleShift)) : 0.f;
+      s8[i] = in ? __ldg(sc.s8 + (col >> F::kScaleShift)) : 0.f;
+    }
+  }
+}
+
 // The columns of the lane's token for one box; `tok` points at the box's first column, `left`
 // columns follow there.  Past the end of a reduction that is no multiple of a box the
 // weights read as zero, and so must the token.
@@ -167,25 +188,7 @@ __device__ __forceinline__ void mac_box(uint32_t boxes, const uint4 (&x)[Format<
     for (int h = 0; h < 2; ++h) {
       float s0[MT][4], s8[MT][4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        if (F::kScaleBoxes && sc[mt].in_box) {
-          const uint32_t at = sc[mt].box + g * 32 + h * 16;
-          const uint4 a = ld_shared_v4(at), b = ld_shared_v4(at + 256);
-          s0[mt][0] = __uint_as_float(a.x), s0[mt][1] = __uint_as_float(a.y);
-          s0[mt][2] = __uint_as_float(a.z), s0[mt][3] = __uint_as_float(a.w);
-          s8[mt][0] = __uint_as_float(b.x), s8[mt][1] = __uint_as_float(b.y);
-          s8[mt][2] = __uint_as_float(b.z), s8[mt][3] = __uint_as_float(b.w);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            // boxes reach past the end of a reduction that is no multiple of theirs: zero weights
-            const int col = 128 * h + 32 * i;
-            const bool in = col < sc[mt].left;
-            s0[mt][i] = in ? __ldg(sc[mt].s0 + (col >> F::kScaleShift)) : 0.f;
-            s8[mt][i] = in ? __ldg(sc[mt].s8 + (col >> F::kScaleShift)) : 0.f;
-          }
-        }
-      }
+      for (int mt = 0; mt < MT; ++mt) load_block_scales<WF>(sc[mt], h, s0[mt], s8[mt]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint4 v = x[4 * h + i];
@@ -205,6 +208,96 @@ __device__ __forceinline__ void mac_box(uint32_t boxes, const uint4 (&x)[Format<
           acc[mt][1] = fmaf(q[1], s0[mt][i], acc[mt][1]);
           acc[mt][2] = fmaf(q[2], s8[mt][i], acc[mt][2]);
           acc[mt][3] = fmaf(q[3], s8[mt][i], acc[mt][3]);
+        }
+      }
+    }
+  }
+}
+
+// The same for several tiles of 8 tokens: every code is widened once for all of them.  The token
+// columns are loaded here, piece by piece: load(nt, i) is the i-th 16-byte piece of the
+// lane's token of tile nt (in load_token's order).
+template <int WF, int MT, int NT, typename Load>
+__device__ __forceinline__ void mac_box_tiles(uint32_t boxes, int ntiles, Load load, const Scales (&sc)[MT],
+                                              float (&acc)[MT][NT][4]) {
+  using F = Format<WF>;
+  const int g = lane_id() >> 2, c = lane_id() & 3;
+  const uint32_t row = boxes + g * 128;
+  if constexpr (!F::kInt4) {
+    constexpr int kHalf = F::kLoads / 2;  // pieces of half a box
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint4 x[NT][kHalf];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i)
+          if (nt < ntiles) x[nt][i] = load(nt, h * kHalf + i);
+      const uint32_t at = row + (((2 * c + h) ^ g) << 4);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const uint4 av = ld_shared_v4(at + mt * kBoxBytes), bv = ld_shared_v4(at + mt * kBoxBytes + 1024);
+        if constexpr (WF == MOE_W_BF16) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            if (nt >= ntiles) break;
+            mma16816(acc[mt][nt], av.x, bv.x, av.y, bv.y, x[nt][0].x, x[nt][0].y);
+            mma16816(acc[mt][nt], av.z, bv.z, av.w, bv.w, x[nt][0].z, x[nt][0].w);
+          }
+        } else {
+          const uint32_t a[4] = {av.x, av.y, av.z, av.w}, b[4] = {bv.x, bv.y, bv.z, bv.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t a0 = widen_int8(a[i]), a1 = widen_int8(b[i]), a2 = widen_int8(a[i] >> 8), a3 = widen_int8(b[i] >> 8);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if (nt >= ntiles) break;
+              const uint4 v = x[nt][i >> 1];
+              const uint32_t lo = (i & 1) ? v.z : v.x, hi = (i & 1) ? v.w : v.y;
+              mma16816(acc[mt][nt], a0, a1, a2, a3, __byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
+            }
+          }
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float s0[MT][4], s8[MT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) load_block_scales<WF>(sc[mt], h, s0[mt], s8[mt]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint4 x[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          if (nt < ntiles) x[nt] = load(nt, 4 * h + i);
+        const uint32_t at = row + (((4 * h + i) ^ g) << 4) + 4 * c;
+        uint32_t wa[MT][4], wb[MT][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const uint32_t a = ld_shared_u32(at + mt * kBoxBytes), b = ld_shared_u32(at + mt * kBoxBytes + 1024);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) wa[mt][k] = widen_int4(a, k), wb[mt][k] = widen_int4(b, k);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if (nt >= ntiles) break;
+          const uint32_t b0 = __byte_perm(x[nt].x, x[nt].z, 0x5410), b1 = __byte_perm(x[nt].x, x[nt].z, 0x7632);
+          const uint32_t b2 = __byte_perm(x[nt].y, x[nt].w, 0x5410), b3 = __byte_perm(x[nt].y, x[nt].w, 0x7632);
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
+          mma16816(d, kMinus24, kMinus24, kMinus24, kMinus24, b0, b1);
+          mma16816(d, kMinus24, kMinus24, kMinus24, kMinus24, b2, b3);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            float q[4];
+            mma16816(q, wa[mt][0], wb[mt][0], wa[mt][1], wb[mt][1], b0, b1, d);
+            mma16816(q, wa[mt][2], wb[mt][2], wa[mt][3], wb[mt][3], b2, b3);
+            acc[mt][nt][0] = fmaf(q[0], s0[mt][i], acc[mt][nt][0]);
+            acc[mt][nt][1] = fmaf(q[1], s0[mt][i], acc[mt][nt][1]);
+            acc[mt][nt][2] = fmaf(q[2], s8[mt][i], acc[mt][nt][2]);
+            acc[mt][nt][3] = fmaf(q[3], s8[mt][i], acc[mt][nt][3]);
+          }
         }
       }
     }
