@@ -1,0 +1,465 @@
+// The dense product for many tokens on the 5th-generation tensor cores.
+//
+// y [M, N] = act(x W^T + b) ...: tokens are the rows of the matrix instruction, outputs its
+// columns.  A pair of CTAs (cta_group::2) computes 256 tokens x 256 columns: each CTA holds 128
+// tokens and 128 rows of W per 64-column stage, 32 KB where a CTA of its own would load
+// 48 KB for the same instructions -- what an SM can take from L2 is the bound that a single
+// CTA's 128 x 256 tile meets first.  Gated, one CTA's rows of W are gate rows and the other's
+// the up rows with the same numbers, so that both of an output's projections end up in the
+// TMEM lane of its token.
+//
+// Roles in each CTA of the persistent pair:
+//   warp 0       TMA: its 128 tokens and its 128 rows of W, signalled to the leader's barrier
+//   warp 1       (leader) tcgen05.mma for both CTAs; commits free the stages of both
+//   warp 2       TMEM
+//   warps 4..11  epilogue from TMEM, two groups of 128 lanes: one accumulator is drained while
+//                the next tile is multiplied into the other
+// Where the tiles are fewer than the pairs, the reduction is split; the splits' fp32 sums are
+// added in order by a second launch with the same epilogue.
+// Quantised weights are widened to bf16 in the workspace first: int8 codes exactly, with the row
+// scale left for the epilogue, int4 as q s rounded once (half a step of bf16 per weight, as the
+// routed layer's tensor-core path has it; the relative error of a sum is below y's own rounding).
+// The pass costs 3 bytes or 2.6 per weight, most of it in L2, against 2 M operations per
+// weight: a few percent from a thousand tokens on.
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "linear.h"
+#include "tmap.h"
+
+namespace moe {
+namespace {
+
+constexpr int kRows = 128;  // tokens, and rows of W, per CTA and stage
+constexpr int kK = 64;      // columns per stage: one 128-byte swizzle row of bf16
+constexpr int kHalf = kRows * kK * 2;
+constexpr int kStage = 2 * kHalf;
+constexpr int kStages = 6;
+constexpr int kTileN = 256;  // columns of the pair's accumulator
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (4 + kEpiWarps);
+constexpr int kSmem = 1024 + kStages * kStage + 512;
+
+struct TcArgs {
+  LinearArgs l;
+  int row_scales;       // int8: the epilogue scales the sums
+  int mt, nt, splits;   // tiles of 256 tokens, of 256 (gated: 128) outputs; parts of the reduction
+  int ksteps;
+  int vec;              // y and residual rows in 16-byte pieces
+  float* partial;       // splits > 1: [splits][1 or 2][M][N]
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the shared address of the leader CTA's copy of a variable
+__device__ __forceinline__ uint32_t leader_addr(const void* p) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+  return r;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// 2-D tile into this CTA's shared memory, completing on a barrier of the pair
+__device__ __forceinline__ void tma_load_pair(void* dst, const void* map, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
+          "r"(smem_u32(dst)),
+      "l"(map), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void umma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// arrive on the barrier at this offset in both CTAs when the MMAs issued so far are done
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                   smem_u32(bar)),
+               "h"((uint16_t)3)
+               : "memory");
+}
+
+struct Tile {
+  int m, n, split;
+};
+// tokens fastest within groups of 8 token tiles, so that the tiles in flight share x and W in L2
+__device__ __forceinline__ Tile tile_of(const TcArgs& a, int t) {
+  Tile r;
+  r.split = t % a.splits;
+  t /= a.splits;
+  const int group = 8 * a.nt, g = t / group, in = t - g * group;
+  const int size = min(8, a.mt - g * 8);
+  r.m = g * 8 + in % size;
+  r.n = in / size;
+  return r;
+}
+
+// 16 outputs of token m from column n0 on
+template <bool GATED>
+__device__ __forceinline__ void finish16(const TcArgs& a, int split, int m, int n0, const uint32_t (&v)[16],
+                                         const uint32_t (&u)[16]) {
+  const LinearArgs& l = a.l;
+  if (a.splits > 1) {
+    float* out = a.partial + (((size_t)split * (GATED ? 2 : 1)) * l.M + m) * l.N + n0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      if (n0 + j >= l.N) break;
+      out[j] = __uint_as_float(v[j]);
+      if (GATED) out[(size_t)l.M * l.N + j] = __uint_as_float(u[j]);
+    }
+    return;
+  }
+  if (!a.vec || n0 + 16 > l.N) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (n0 + j < l.N) linear_finish(l, a.row_scales, m, n0 + j, __uint_as_float(v[j]), GATED ? __uint_as_float(u[j]) : 0.f);
+    return;
+  }
+  float y[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    float s = __uint_as_float(v[j]);
+    if (a.row_scales) s *= __ldg(l.s[0] + n0 + j);
+    if (l.b[0]) s += __ldg(l.b[0] + n0 + j);
+    // outputs in bf16: the fast forms, a few units in the last place of fp32
+    const bool fast = l.yfmt == MOE_X_BF16;
+    if (l.act == MOE_ACT_SILU) s = fast ? silu_mul_fast(s, 1.f) : silu_mul(s, 1.f);
+    if (l.act == MOE_ACT_GELU_TANH) s = fast ? gelu_tanh_mul_fast(s, 1.f) : gelu_tanh_mul(s, 1.f);
+    if (GATED) {
+      float g = __uint_as_float(u[j]);
+      if (a.row_scales) g *= __ldg(l.s[1] + n0 + j);
+      if (l.b[1]) g += __ldg(l.b[1] + n0 + j);
+      s *= g;
+    }
+    y[j] = s;
+  }
+  if (l.yfmt == MOE_X_BF16) {
+    uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(l.y) + (size_t)m * l.ldy + n0);
+    if (l.residual) {
+      const uint4* r = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(l.residual) + (size_t)m * l.ldr + n0);
+      const uint4 r0 = r[0], r1 = r[1];
+      const uint32_t rr[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        y[2 * j] += bf16_to_f32(rr[j] & 0xFFFFu);
+        y[2 * j + 1] += __uint_as_float(rr[j] & 0xFFFF0000u);
+      }
+    }
+    uint32_t o[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = pack_bf16x2(y[2 * j], y[2 * j + 1]);
+    out[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  } else {
+    float4* out = reinterpret_cast<float4*>(static_cast<float*>(l.y) + (size_t)m * l.ldy + n0);
+    const float* r = static_cast<const float*>(l.residual);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float4 o = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+      if (r) {
+        const float4 e = *reinterpret_cast<const float4*>(r + (size_t)m * l.ldr + n0 + 4 * j);
+        o.x += e.x, o.y += e.y, o.z += e.z, o.w += e.w;
+      }
+      out[j] = o;
+    }
+  }
+}
+
+template <bool GATED>
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+    linear_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w0,
+                     const __grid_constant__ CUtensorMap map_w1, const __grid_constant__ TcArgs a, uint32_t* flags) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStage);  // leader's: both CTAs' stage has landed
+  uint64_t* empty = full + kStages;                                       // the MMAs have read the stage
+  uint64_t* acc_full = empty + kStages;                                   // [2]
+  uint64_t* acc_empty = acc_full + 2;                                     // [2] leader's: both CTAs have drained it
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  const int w = warp_id(), lane = lane_id();
+  const uint32_t rank = cluster_rank();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 2 * kEpiWarps);
+    }
+    fence_mbar_init();
+    prefetch_tmap(&map_x);
+    prefetch_tmap(rank && GATED ? &map_w1 : &map_w0);
+  }
+  if (w == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    tc_fence_before();
+  }
+  __syncthreads();
+  cluster_sync();  // the peer's barriers are initialised
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+
+  const int tiles = a.mt * a.nt * a.splits, pairs = (int)gridDim.x / 2, pair = (int)blockIdx.x / 2;
+  auto steps_of = [&](int split, int& k0) {
+    k0 = (int)((long long)split * a.ksteps / a.splits);
+    return (int)((long long)(split + 1) * a.ksteps / a.splits) - k0;
+  };
+  auto wait = [&](uint64_t* bar, uint32_t parity, bool& dead) {
+    if (dead) return;
+    if (!mbar_wait(bar, parity)) {
+      dead = true;
+      raise_flag(flags, MOE_FLAG_TIMEOUT);
+    }
+  };
+
+  if (w == 0) {
+    if (lane == 0) {
+      bool dead = false;
+      uint32_t it = 0;
+      const CUtensorMap* map_w = GATED && rank ? &map_w1 : &map_w0;
+      for (int t = pair; t < tiles && !dead; t += pairs) {
+        const Tile tl = tile_of(a, t);
+        int k0;
+        const int nk = steps_of(tl.split, k0);
+        const int row_x = tl.m * 2 * kRows + (int)rank * kRows;
+        const int row_w = GATED ? tl.n * kRows : tl.n * 2 * kRows + (int)rank * kRows;
+        for (int k = 0; k < nk; ++k, ++it) {
+          const int s = it % kStages;
+          wait(&empty[s], ((it / kStages) & 1u) ^ 1u, dead);
+          if (dead) break;
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStage);
+          const uint32_t bar = leader_addr(&full[s]);
+          uint8_t* stage = smem + s * kStage;
+          tma_load_pair(stage, &map_x, (k0 + k) * kK, row_x, bar);
+          tma_load_pair(stage + kHalf, map_w, (k0 + k) * kK, row_w, bar);
+        }
+      }
+      // after a wait that ran out: the copies in flight end before the pair leaves
+      if (dead && rank == 0)
+        for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i) mbar_wait(&full[i % kStages], (i / kStages) & 1u);
+    }
+  } else if (w == 1) {
+    if (rank == 0 && lane == 0) {
+      bool dead = false;
+      uint32_t it = 0, n = 0;
+      const uint32_t idesc = umma_idesc_bf16(2 * kRows, kTileN);
+      for (int t = pair; t < tiles && !dead; t += pairs, ++n) {
+        const Tile tl = tile_of(a, t);
+        int k0;
+        const int nk = steps_of(tl.split, k0);
+        const uint32_t buf = n & 1u, d = tmem + buf * kTileN;
+        wait(&acc_empty[buf], ((n >> 1) & 1u) ^ 1u, dead);
+        tc_fence_after();
+        for (int k = 0; k < nk && !dead; ++k, ++it) {
+          const int s = it % kStages;
+          wait(&full[s], (it / kStages) & 1u, dead);
+          if (dead) break;
+          tc_fence_after();
+          const uint32_t stage = smem_u32(smem + s * kStage);
+#pragma unroll
+          for (int j = 0; j < kK / 16; ++j)
+            umma_pair(d, umma_desc_sw128(stage + 32 * j), umma_desc_sw128(stage + kHalf + 32 * j), idesc, (k | j) != 0);
+          commit_pair(&empty[s]);
+        }
+        if (!dead) commit_pair(&acc_full[buf]);
+      }
+    }
+  } else if (w >= 4) {
+    const int q = w & 3, group = (w - 4) >> 2;  // lane quarter; half of the columns
+    constexpr int kCols = GATED ? kTileN / 4 : kTileN / 2;  // outputs of a group
+    const int outs = GATED ? kRows : 2 * kRows;             // outputs of a tile
+    const LinearArgs& l = a.l;
+    bool dead = false;
+    uint32_t n = 0;
+    for (int t = pair; t < tiles; t += pairs, ++n) {
+      const Tile tl = tile_of(a, t);
+      const uint32_t buf = n & 1u;
+      wait(&acc_full[buf], (n >> 1) & 1u, dead);
+      dead = __any_sync(0xFFFFFFFFu, dead);
+      if (dead) break;
+      tc_fence_after();
+      const int m = tl.m * 2 * kRows + (int)rank * kRows + q * 32 + lane;
+      const int c_first = tl.n * outs + group * kCols;
+      const uint32_t at = tmem + buf * kTileN + ((uint32_t)(q * 32) << 16) + group * kCols;
+#pragma unroll 1
+      for (int c = 0; c < kCols; c += 16) {
+        uint32_t v[16], u[16];
+        __syncwarp();
+        tmem_ld16(at + c, v);
+        if (GATED) tmem_ld16(at + kTileN / 2 + c, u);
+        tmem_ld_wait();
+        if (m < l.M) finish16<GATED>(a, tl.split, m, c_first + c, v, u);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(leader_addr(&acc_empty[buf]));
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  __syncwarp();
+  cluster_sync();  // the peer's MMAs have read this CTA's shared memory, its drains this TMEM
+  if (w == 2) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+// the splits' sums in order, then the epilogue
+__global__ void __launch_bounds__(256) linear_sum_kernel(const __grid_constant__ TcArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const LinearArgs& l = a.l;
+  const size_t n = (size_t)l.M * l.N, parts = l.W[1] ? 2 : 1;
+  for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (size_t)gridDim.x * blockDim.x) {
+    float v = 0.f, u = 0.f;
+    for (int s = 0; s < a.splits; ++s) {
+      v += a.partial[s * parts * n + i];
+      if (parts == 2) u += a.partial[(s * parts + 1) * n + i];
+    }
+    linear_finish(l, a.row_scales, (int)(i / l.N), (int)(i % l.N), v, u);
+  }
+}
+
+// 16 stored weights per thread and step to bf16
+template <int WF>
+__global__ void __launch_bounds__(256) linear_widen_kernel(const void* __restrict__ W, const float* __restrict__ s, size_t n16,
+                                                           int K, uint16_t* __restrict__ out) {
+  pdl_wait();
+  pdl_trigger();
+  for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n16; i += (size_t)gridDim.x * blockDim.x) {
+    uint32_t o[8];
+    if constexpr (WF == MOE_W_INT8_ROW) {
+      const uint4 q = ldg_stream(static_cast<const uint8_t*>(W) + 16 * i);
+      const uint32_t word[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t two = word[j >> 1] >> (16 * (j & 1));
+        o[j] = pack_bf16x2((float)(int8_t)two, (float)(int8_t)(two >> 8));
+      }
+    } else {
+      constexpr int kShift = WF == MOE_W_INT4_B32 ? 5 : 7;
+      const uint2 q = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(W) + 8 * i));
+      const float scale = __ldg(s + ((16 * i) >> kShift));  // K is a multiple of the block: blocks do not cross rows
+      const uint32_t word[2] = {q.x, q.y};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t two = word[j >> 2] >> (8 * (j & 3));
+        o[j] = pack_bf16x2((float)((int)(two << 28) >> 28) * scale, (float)((int)(two << 24) >> 28) * scale);
+      }
+    }
+    uint4* to = reinterpret_cast<uint4*>(out + 16 * i);
+    to[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    to[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+struct TcLayout {
+  int mt, nt, ksteps, splits;
+  size_t w[2], partial, total;  // offsets in the workspace
+};
+TcLayout tc_layout(const moe_linear_desc& d, int M) {
+  TcLayout t;
+  const bool gated = d.W_up != nullptr;
+  const int outs = gated ? kRows : 2 * kRows;
+  t.mt = (M + 2 * kRows - 1) / (2 * kRows);
+  t.nt = (d.N + outs - 1) / outs;
+  t.ksteps = (d.K + kK - 1) / kK;
+  // 74 pairs of SMs: split the reduction while the tiles leave half of them idle and a part
+  // keeps 8 stages (the pipeline's fill) to work on
+  t.splits = 1;
+  while ((long long)t.mt * t.nt * t.splits * 2 <= 74 && t.ksteps >= 16 * t.splits) t.splits *= 2;
+  const size_t wide = d.wfmt == MOE_W_BF16 ? 0 : up256((size_t)d.N * d.K * 2);
+  t.w[0] = 0;
+  t.w[1] = wide;
+  t.partial = wide * (gated ? 2 : 1);
+  t.total = t.partial + (t.splits > 1 ? (size_t)t.splits * (gated ? 2 : 1) * M * d.N * 4 : 0);
+  return t;
+}
+
+}  // namespace
+
+bool linear_tc_ok(const moe_linear_desc& d, int M) {
+  return d.xfmt == MOE_X_BF16 && d.wfmt != MOE_W_F32 && M > kLinearStreamTokens;
+}
+
+size_t linear_tc_workspace(const moe_linear_desc& d, int M) { return tc_layout(d, M).total; }
+
+cudaError_t launch_linear_widen(const moe_linear_desc& d, int M, int which, void* workspace, int num_sms, cudaStream_t s) {
+  const TcLayout t = tc_layout(d, M);
+  const void* W = which ? d.W_up : d.W;
+  const float* sc = which ? d.s_up : d.s;
+  uint16_t* out = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + t.w[which]);
+  const size_t n16 = (size_t)d.N * d.K / 16;
+  const dim3 grid((unsigned)std::min<size_t>((n16 + 255) / 256, (size_t)num_sms * 8)), block(256);
+  switch (d.wfmt) {
+    case MOE_W_INT8_ROW: return launch_k(linear_widen_kernel<MOE_W_INT8_ROW>, grid, block, 0, s, W, sc, n16, d.K, out);
+    case MOE_W_INT4_B32: return launch_k(linear_widen_kernel<MOE_W_INT4_B32>, grid, block, 0, s, W, sc, n16, d.K, out);
+    default: return launch_k(linear_widen_kernel<MOE_W_INT4_B128>, grid, block, 0, s, W, sc, n16, d.K, out);
+  }
+}
+
+static TcArgs tc_args(const moe_linear_desc& d, const LinearArgs& a, const TcLayout& t, void* workspace) {
+  TcArgs p = {};
+  p.l = a;
+  p.row_scales = d.wfmt == MOE_W_INT8_ROW;
+  p.mt = t.mt, p.nt = t.nt, p.splits = t.splits, p.ksteps = t.ksteps;
+  const int yb = d.yfmt == MOE_X_F32 ? 4 : 2;
+  auto pieces = [&](const void* q, long long ld) { return reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld * yb % 16 == 0; };
+  p.vec = pieces(a.y, a.ldy) && (!a.residual || pieces(a.residual, a.ldr));
+  p.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + t.partial);
+  return p;
+}
+
+cudaError_t launch_linear_tc(const moe_linear_desc& d, const LinearArgs& a, void* workspace, int num_sms, uint32_t* flags,
+                             cudaStream_t s) {
+  const TcLayout t = tc_layout(d, a.M);
+  const TcArgs p = tc_args(d, a, t, workspace);
+  const bool gated = d.W_up != nullptr;
+  CUtensorMap mx, mw[2];
+  cudaError_t e = make_tmap(&mx, a.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (uint64_t)d.K, (uint64_t)a.M, (uint64_t)a.ldx * 2, kK,
+                            kRows, CU_TENSOR_MAP_SWIZZLE_128B);
+  for (int i = 0; i < (gated ? 2 : 1) && e == cudaSuccess; ++i) {
+    const void* W = d.wfmt == MOE_W_BF16 ? a.W[i] : static_cast<char*>(workspace) + t.w[i];
+    e = make_tmap(&mw[i], W, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (uint64_t)d.K, (uint64_t)d.N, (uint64_t)d.K * 2, kK, kRows,
+                  CU_TENSOR_MAP_SWIZZLE_128B);
+  }
+  if (!gated) mw[1] = mw[0];
+  auto kernel = gated ? linear_tc_kernel<true> : linear_tc_kernel<false>;
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  const long long tiles = (long long)t.mt * t.nt * t.splits;
+  const int pairs = (int)std::min<long long>(tiles, num_sms / 2);
+  return launch_k(kernel, dim3(2 * pairs), dim3(kThreads), kSmem, s, mx, mw[0], mw[1], p, flags);
+}
+
+bool linear_tc_split(const moe_linear_desc& d, int M) { return tc_layout(d, M).splits > 1; }
+
+cudaError_t launch_linear_sum(const moe_linear_desc& d, const LinearArgs& a, void* workspace, int num_sms, cudaStream_t s) {
+  const TcArgs p = tc_args(d, a, tc_layout(d, a.M), workspace);
+  const size_t n = (size_t)a.M * a.N;
+  return launch_k(linear_sum_kernel, dim3((unsigned)std::min<size_t>((n + 255) / 256, (size_t)num_sms * 8)), dim3(256), 0, s, p);
+}
+
+}  // namespace moe

@@ -670,9 +670,7 @@ static moe_status validate_linear(const moe_linear_desc* d, int32_t M) {
 }
 
 size_t moe::linear_workspace_bytes(const moe_linear_desc& d, int M) {
-  (void)d;
-  (void)M;
-  return 0;
+  return linear_tc_ok(d, M) ? linear_tc_workspace(d, M) : 0;
 }
 
 extern "C" moe_status moe_linear_workspace_size(const moe_linear_desc* d, int32_t M, size_t* bytes) {
@@ -711,6 +709,15 @@ extern "C" moe_status moe_linear(const moe_linear_desc* d, const void* x, int64_
   a.W[0] = d->W, a.W[1] = d->W_up, a.s[0] = d->s, a.s[1] = d->s_up, a.b[0] = d->b, a.b[1] = d->b_up;
   if (linear_stream_ok(*d, M)) {
     MOE_LAUNCH("linear_stream", stream, launch_linear_stream(*d, a, dev->num_sms, dev->flags, stream));
+    return MOE_OK;
+  }
+  if (linear_tc_ok(*d, M)) {
+    if (d->wfmt != MOE_W_BF16)
+      for (int i = 0; i < (d->W_up ? 2 : 1); ++i)
+        MOE_LAUNCH("linear_widen", stream, launch_linear_widen(*d, M, i, workspace, dev->num_sms, stream));
+    MOE_LAUNCH("linear_tc", stream, launch_linear_tc(*d, a, workspace, dev->num_sms, dev->flags, stream));
+    if (linear_tc_split(*d, M))
+      MOE_LAUNCH("linear_sum", stream, launch_linear_sum(*d, a, workspace, dev->num_sms, stream));
     return MOE_OK;
   }
   MOE_LAUNCH("linear_simt", stream, launch_linear_simt(*d, a, stream));
