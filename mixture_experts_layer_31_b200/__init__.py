@@ -310,21 +310,15 @@ def _require(ok: bool, message: str):
         raise MoeError(MOE_ERR_INVALID_ARG, message)
 
 
-class _OnDevice:
-    """Makes `device` current for a call, where it is not already."""
+def _fits(t, dtype, rows: int, cols: int, device) -> bool:
+    """A [rows, cols] tensor of the dtype on the device, its rows contiguous."""
+    return (t.dtype == dtype and t.dim() == 2 and t.shape[0] == rows and t.shape[1] == cols
+            and (cols == 1 or t.stride(1) == 1) and t.device == device)
 
-    def __init__(self, torch, device):
-        self.torch, self.index, self.guard = torch, device.index, None
 
-    def __enter__(self):
-        if self.index is not None and self.index != self.torch.cuda.current_device():
-            self.guard = self.torch.cuda.device(self.index)
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            guard, self.guard = self.guard, None
-            guard.__exit__(*exc)
+def _raw_stream(torch, device) -> int:
+    """The current stream of a CUDA device, as the library takes it."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 class MoELayer:
@@ -468,28 +462,33 @@ class MoELayer:
         `out` = (y, idx, w) if given (y may be residual itself).  Calls on one stream share a
         workspace that the layer keeps; so do the graphs captured on one stream: replay
         those in order, or capture them from layers of their own."""
-        torch, d = self.torch, self.desc
+        torch, d, device = self.torch, self.desc, self.tensors["W_r"].device
+        H, k, dtype = d.H, d.k, self.x_dtype
         T = x.shape[0]
-        with _OnDevice(torch, x.device):
-            if out is None:
-                out = (torch.empty((T, d.H), dtype=self.x_dtype, device=x.device),
-                       torch.empty((T, d.k), dtype=torch.int32, device=x.device),
-                       torch.empty((T, d.k), dtype=torch.float32, device=x.device))
-            y, idx, w = out
-            for t, n, dtype, name in ((x, d.H, self.x_dtype, "x"), (y, d.H, self.x_dtype, "y"),
-                                      (idx, d.k, torch.int32, "idx"), (w, d.k, torch.float32, "w"),
-                                      (residual, d.H, self.x_dtype, "residual")):
-                if t is not None:
-                    _require(t.dtype == dtype and t.shape == (T, n) and t.is_contiguous() and t.device == x.device,
-                             "%s must be a contiguous %s tensor [%d, %d] on x's device" % (name, dtype, T, n))
-            _require(x.device.type == "cuda" and x.device == self.tensors["W_r"].device,
-                     "x must be on the layer's device")
-            stream = torch.cuda.current_stream(x.device).cuda_stream
-            ws = self.few_workspace(T, stream)
-            moe_few_forward(d, self.shared, x.data_ptr(), T, idx.data_ptr(), w.data_ptr(),
-                            None if residual is None else residual.data_ptr(), y.data_ptr(), ws.data_ptr(),
-                            ws.numel(), stream)
-        return y, idx, w
+        _require(device.type == "cuda" and _fits(x, dtype, T, H, device) and x.is_contiguous(),
+                 "x must be a contiguous %s tensor [T, %d] on the layer's GPU" % (dtype, H))
+        if device.index != torch._C._cuda_getDevice():
+            with torch.cuda.device(device):
+                return self.few(x, residual, out)
+        if out is None:
+            out = (torch.empty((T, H), dtype=dtype, device=device), torch.empty((T, k), dtype=torch.int32, device=device),
+                   torch.empty((T, k), dtype=torch.float32, device=device))
+        y, idx, w = out
+        _require(_fits(y, dtype, T, H, device) and y.is_contiguous() and _fits(idx, torch.int32, T, k, device)
+                 and idx.is_contiguous() and _fits(w, torch.float32, T, k, device) and w.is_contiguous(),
+                 "out must be contiguous tensors y [T, H], idx [T, k] int32 and w [T, k] float32 on x's device")
+        r = None
+        if residual is not None:
+            _require(_fits(residual, dtype, T, H, device) and residual.is_contiguous(),
+                     "residual must be a contiguous %s tensor [%d, %d] on x's device" % (dtype, T, H))
+            r = residual.data_ptr()
+        stream = _raw_stream(torch, device)
+        ws = self.few_workspace(T, stream)
+        st = lib().moe_few_forward(ctypes.byref(d), None if self.shared is None else ctypes.byref(self.shared), x.data_ptr(),
+                                   T, idx.data_ptr(), w.data_ptr(), r, y.data_ptr(), ws.data_ptr(), ws.numel(), stream)
+        if st:
+            _check(st)
+        return out
 
     def expert_counts(self, idx, counts=None):
         """Accumulate per-expert routing counts of idx [T, k] into counts (a device
@@ -528,10 +527,13 @@ class Linear:
         self.x_dtype = torch.bfloat16 if d.xfmt == MOE_X_BF16 else torch.float32
         self.y_dtype = torch.bfloat16 if d.yfmt == MOE_X_BF16 else torch.float32
         self._ws = {}
+        self._need = {}  # workspace bytes by M
 
     def workspace(self, M: int, stream: int = 0):
         """The workspace of the calls on one stream (they run in order and share it)."""
-        n = moe_linear_workspace_size(self.desc, M)
+        n = self._need.get(M)
+        if n is None:
+            n = self._need[M] = moe_linear_workspace_size(self.desc, M)
         ws = self._ws.get(stream)
         if ws is None or ws.numel() < n:
             ws = self._ws[stream] = self.torch.empty(max(n, 256), dtype=self.torch.uint8,
@@ -543,26 +545,28 @@ class Linear:
         with contiguous rows; y may be residual itself.  Calls on one stream share a workspace
         that the object keeps; so do the graphs captured on one stream: replay those in
         order, or capture them from objects of their own."""
-        torch, d = self.torch, self.desc
+        torch, d, device = self.torch, self.desc, self.tensors["W"].device
+        K, N, dtype = d.K, d.N, self.y_dtype
         M = x.shape[0]
-        with _OnDevice(torch, x.device):
-            if y is None:
-                y = torch.empty((M, d.N), dtype=self.y_dtype, device=x.device)
-            for t, n, dtype, name in ((x, d.K, self.x_dtype, "x"), (y, d.N, self.y_dtype, "y"),
-                                      (residual, d.N, self.y_dtype, "residual")):
-                if t is not None:
-                    _require(t.dtype == dtype and t.shape == (M, n) and t.device == x.device
-                             and (n == 1 or t.stride(1) == 1),
-                             "%s must be a %s tensor [%d, %d] with contiguous rows on x's device" % (name, dtype, M, n))
-            _require(x.device.type == "cuda" and x.device == self.tensors["W"].device,
-                     "x must be on the weights' device")
-
-            def ld(t, n):
-                return t.stride(0) if M > 1 else n
-
-            stream = torch.cuda.current_stream(x.device).cuda_stream
-            ws = self.workspace(M, stream)
-            moe_linear(d, x.data_ptr(), ld(x, d.K), M, None if residual is None else residual.data_ptr(),
-                       0 if residual is None else ld(residual, d.N), y.data_ptr(), ld(y, d.N), ws.data_ptr(),
-                       ws.numel(), stream)
+        _require(device.type == "cuda" and _fits(x, self.x_dtype, M, K, device),
+                 "x must be a %s tensor [M, %d] with contiguous rows on the weights' GPU" % (self.x_dtype, K))
+        if device.index != torch._C._cuda_getDevice():
+            with torch.cuda.device(device):
+                return self(x, residual, y)
+        if y is None:
+            y = torch.empty((M, N), dtype=dtype, device=device)
+        else:
+            _require(_fits(y, dtype, M, N, device),
+                     "y must be a %s tensor [%d, %d] with contiguous rows on x's device" % (dtype, M, N))
+        r, ldr = None, 0
+        if residual is not None:
+            _require(_fits(residual, dtype, M, N, device),
+                     "residual must be a %s tensor [%d, %d] with contiguous rows on x's device" % (dtype, M, N))
+            r, ldr = residual.data_ptr(), residual.stride(0) if M > 1 else N
+        stream = _raw_stream(torch, device)
+        ws = self.workspace(M, stream)
+        st = lib().moe_linear(ctypes.byref(d), x.data_ptr(), x.stride(0) if M > 1 else K, M, r, ldr, y.data_ptr(),
+                              y.stride(0) if M > 1 else N, ws.data_ptr(), ws.numel(), stream)
+        if st:
+            _check(st)
         return y

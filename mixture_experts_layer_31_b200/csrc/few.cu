@@ -980,8 +980,8 @@ cudaError_t launch_stream(FewArgs a, int num_sms, cudaStream_t s) {
       e = weight_maps<WF>(&m.ws[i], &m.ss[i], a.Ws[i], a.ss[i], (uint64_t)(i < 2 ? a.Is : a.H), i < 2 ? a.H : a.Is,
                           a.boxed[2 + i / 2]);
   }
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(few_stream_kernel<WF>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<bool> allowed[64];
+  if (e == cudaSuccess) e = allow_smem(reinterpret_cast<const void*>(few_stream_kernel<WF>), smem, allowed);
   if (e != cudaSuccess) return e;
   // cooperative: the grid's barrier needs every CTA resident (one per SM)
   return launch_k_cooperative(few_stream_kernel<WF>, dim3(num_sms), dim3(kStreamThreads), smem, s, m, a);

@@ -4,6 +4,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "moe.h"
 
 namespace moe {
@@ -52,6 +54,18 @@ cudaError_t launch_k_cooperative(void (*kernel)(KArgs...), dim3 grid, dim3 block
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// Lets a kernel use `smem` bytes of dynamic shared memory, once per device (the current one).
+// `done` is the kernel's own array.
+inline cudaError_t allow_smem(const void* kernel, size_t smem, std::atomic<bool> (&done)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_relaxed);
+  return e;
 }
 
 // Tokens are routed in chunks of this many (token, slot) pairs when building

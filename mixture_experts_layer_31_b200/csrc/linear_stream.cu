@@ -210,7 +210,8 @@ cudaError_t launch(const moe_linear_desc& d, const LinearArgs& a, int num_sms, u
                     (uint64_t)(d.K / 32) * 4, 8, stream::kBoxRows, CU_TENSOR_MAP_SWIZZLE_NONE);
   }
   auto kernel = linear_stream_kernel<WF, MT, NT>;
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kBytes);
+  static std::atomic<bool> allowed[64];
+  if (e == cudaSuccess) e = allow_smem(reinterpret_cast<const void*>(kernel), P::kBytes, allowed);
   if (e != cudaSuccess) return e;
   const int rows = gated ? 16 : 16 * MT, units = (d.N + rows - 1) / rows;
   return launch_k(kernel, dim3(std::min(units, num_sms)), dim3(kThreads), P::kBytes, s, m, p, flags);

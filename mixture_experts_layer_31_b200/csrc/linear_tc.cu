@@ -447,7 +447,8 @@ cudaError_t launch_linear_tc(const moe_linear_desc& d, const LinearArgs& a, void
   }
   if (!gated) mw[1] = mw[0];
   auto kernel = gated ? linear_tc_kernel<true> : linear_tc_kernel<false>;
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  static std::atomic<bool> allowed[2][64];
+  if (e == cudaSuccess) e = allow_smem(reinterpret_cast<const void*>(kernel), kSmem, allowed[gated]);
   if (e != cudaSuccess) return e;
   const long long tiles = (long long)t.mt * t.nt * t.splits;
   const int pairs = (int)std::min<long long>(tiles, num_sms / 2);
