@@ -49,16 +49,19 @@ __device__ __forceinline__ void linear_finish(const LinearArgs& a, bool row_scal
 
 bool linear_stream_ok(const moe_linear_desc& d, int M);
 cudaError_t launch_linear_stream(const moe_linear_desc& d, const LinearArgs& a, int num_sms, uint32_t* flags, cudaStream_t s);
-// beyond that, tensor cores: quantised weights are first widened into the workspace (one launch per
-// matrix), and where linear_tc_split() a last launch adds up the parts
+// fp32 tokens or weights: up to this many tokens a warp computes rows of W in fp32
+constexpr int kLinearRowTokens = 16;
+cudaError_t launch_linear_rows(const moe_linear_desc& d, const LinearArgs& a, int num_sms, cudaStream_t s);
+// beyond that, tensor cores: quantised and fp32 weights are first widened into bf16 (parts) in the
+// workspace, one launch per matrix, fp32 tokens likewise; where linear_tc_split() a last launch
+// adds up the parts of the reduction
 bool linear_tc_ok(const moe_linear_desc& d, int M);
 size_t linear_tc_workspace(const moe_linear_desc& d, int M);
 bool linear_tc_split(const moe_linear_desc& d, int M);
 cudaError_t launch_linear_widen(const moe_linear_desc& d, int M, int which, void* workspace, int num_sms, cudaStream_t s);
+cudaError_t launch_linear_split_x(const moe_linear_desc& d, const LinearArgs& a, void* workspace, int num_sms, cudaStream_t s);
 cudaError_t launch_linear_tc(const moe_linear_desc& d, const LinearArgs& a, void* workspace, int num_sms, uint32_t* flags,
                              cudaStream_t s);
 cudaError_t launch_linear_sum(const moe_linear_desc& d, const LinearArgs& a, void* workspace, int num_sms, cudaStream_t s);
-// everything else: fp32 weights or tokens
-cudaError_t launch_linear_simt(const moe_linear_desc& d, const LinearArgs& a, cudaStream_t s);
 
 }  // namespace moe

@@ -16,6 +16,13 @@
 //                the next tile is multiplied into the other
 // Where the tiles are fewer than the pairs, the reduction is split; the splits' fp32 sums are
 // added in order by a second launch with the same epilogue.
+// fp32 operands go through the same instructions in three bf16 parts, x = h + m + l with 8
+// significant bits each, exactly: the products of parts that matter to 24 bits (six of two
+// fp32 operands, three where one is exact in bf16) are summed, the small ones first; what is
+// left out is below 2^-23 of each product.  That is six times the operations of a bf16
+// product and still several times the rate of fp32 multiply-adds.  The tensor core's own
+// additions round towards zero, so long reductions are split and the parts' sums added in
+// fp32 (kF32Steps).
 // Quantised weights are widened to bf16 in the workspace first: int8 codes exactly, with the row
 // scale left for the epilogue, int4 as q s rounded once (half a step of bf16 per weight, as the
 // routed layer's tensor-core path has it; the relative error of a sum is below y's own rounding).
@@ -41,16 +48,31 @@ constexpr int kStages = 6;
 constexpr int kTileN = 256;  // columns of the pair's accumulator
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (4 + kEpiWarps);
-constexpr int kSmem = 1024 + kStages * kStage + 512;
+constexpr int kTurn = 32 * 17 * 4;  // a warp's 32 x 16 results, turned from a row a lane to a row at a time
+constexpr int kSmem = 1024 + kStages * kStage + 512 + kEpiWarps * kTurn;
 
 struct TcArgs {
   LinearArgs l;
   int row_scales;       // int8: the epilogue scales the sums
   int mt, nt, splits;   // tiles of 256 tokens, of 256 (gated: 128) outputs; parts of the reduction
   int ksteps;
+  int xparts, wparts;   // bf16 parts of x and of W: 1, or 3 of an fp32 operand (its rows follow one another)
   int vec;              // y and residual rows in 16-byte pieces
-  float* partial;       // splits > 1: [splits][1 or 2][M][N]
+  float* partial;       // splits > 1: [splits][1 or 2][M][np]
+  int np;               // N rounded up to 16
 };
+
+// the products of parts, least first: (part of x, part of W)
+struct Parts {
+  int x, w;
+};
+__device__ __forceinline__ int products(int xp, int wp) { return xp == 1 ? wp : (wp == 1 ? xp : 6); }
+__device__ __forceinline__ Parts product(int xp, int wp, int i) {
+  if (wp == 1) return Parts{xp - 1 - i, 0};
+  if (xp == 1) return Parts{0, wp - 1 - i};
+  // (2, 0) (0, 2) (1, 1) (1, 0) (0, 1) (0, 0)
+  return Parts{(0x001102 >> (4 * i)) & 15, (0x010120 >> (4 * i)) & 15};
+}
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -114,19 +136,13 @@ __device__ __forceinline__ void finish16(const TcArgs& a, int split, int m, int 
                                          const uint32_t (&u)[16]) {
   const LinearArgs& l = a.l;
   if (a.splits > 1) {
-    float* out = a.partial + (((size_t)split * (GATED ? 2 : 1)) * l.M + m) * l.N + n0;
+    if (n0 >= a.np) return;
+    uint4* out = reinterpret_cast<uint4*>(a.partial + (((size_t)split * (GATED ? 2 : 1)) * l.M + m) * a.np + n0);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      if (n0 + j >= l.N) break;
-      out[j] = __uint_as_float(v[j]);
-      if (GATED) out[(size_t)l.M * l.N + j] = __uint_as_float(u[j]);
+    for (int j = 0; j < 4; ++j) {
+      out[j] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      if (GATED) out[(size_t)l.M * a.np / 4 + j] = make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
     }
-    return;
-  }
-  if (!a.vec || n0 + 16 > l.N) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      if (n0 + j < l.N) linear_finish(l, a.row_scales, m, n0 + j, __uint_as_float(v[j]), GATED ? __uint_as_float(u[j]) : 0.f);
     return;
   }
   float y[16];
@@ -238,18 +254,22 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       for (int t = pair; t < tiles && !dead; t += pairs) {
         const Tile tl = tile_of(a, t);
         int k0;
-        const int nk = steps_of(tl.split, k0);
+        const int nk = steps_of(tl.split, k0), all = nk * products(a.xparts, a.wparts);
         const int row_x = tl.m * 2 * kRows + (int)rank * kRows;
         const int row_w = GATED ? tl.n * kRows : tl.n * 2 * kRows + (int)rank * kRows;
-        for (int k = 0; k < nk; ++k, ++it) {
+        int k = 0, i = 0;
+        Parts p = product(a.xparts, a.wparts, 0);
+        for (int n = 0; n < all; ++n, ++it) {
           const int s = it % kStages;
           wait(&empty[s], ((it / kStages) & 1u) ^ 1u, dead);
           if (dead) break;
           if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStage);
           const uint32_t bar = leader_addr(&full[s]);
           uint8_t* stage = smem + s * kStage;
-          tma_load_pair(stage, &map_x, (k0 + k) * kK, row_x, bar);
-          tma_load_pair(stage + kHalf, map_w, (k0 + k) * kK, row_w, bar);
+          // a tile's last rows may be the next part's first: rows past M and N are not used
+          tma_load_pair(stage, &map_x, (k0 + k) * kK, row_x + p.x * a.l.M, bar);
+          tma_load_pair(stage + kHalf, map_w, (k0 + k) * kK, row_w + p.w * a.l.N, bar);
+          if (++k == nk) k = 0, p = product(a.xparts, a.wparts, ++i);
         }
       }
       // after a wait that ran out: the copies in flight end before the pair leaves
@@ -264,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       for (int t = pair; t < tiles && !dead; t += pairs, ++n) {
         const Tile tl = tile_of(a, t);
         int k0;
-        const int nk = steps_of(tl.split, k0);
+        const int nk = steps_of(tl.split, k0) * products(a.xparts, a.wparts);
         const uint32_t buf = n & 1u, d = tmem + buf * kTileN;
         wait(&acc_empty[buf], ((n >> 1) & 1u) ^ 1u, dead);
         tc_fence_after();
@@ -306,7 +326,33 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         tmem_ld16(at + c, v);
         if (GATED) tmem_ld16(at + kTileN / 2 + c, u);
         tmem_ld_wait();
-        if (m < l.M) finish16<GATED>(a, tl.split, m, c_first + c, v, u);
+        const int n0 = c_first + c;
+        if (a.splits > 1 || (a.vec && n0 + 16 <= l.N)) {
+          if (m < l.M) finish16<GATED>(a, tl.split, m, n0, v, u);
+          continue;
+        }
+        // rows of y that 16-byte pieces do not fit: two rows at a time, 16 columns each
+        float* turn = reinterpret_cast<float*>(smem + kStages * kStage + 512 + (w - 4) * kTurn);
+        float g[16];
+#pragma unroll
+        for (int p = 0; p < (GATED ? 2 : 1); ++p) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) turn[lane * 17 + j] = __uint_as_float(p ? u[j] : v[j]);
+          __syncwarp();
+          if (GATED && p == 0) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) g[i] = turn[(2 * i + (lane >> 4)) * 17 + (lane & 15)];
+            __syncwarp();
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int r = 2 * i + (lane >> 4), n = n0 + (lane & 15);
+          const float f = turn[r * 17 + (lane & 15)];
+          const int row = m - lane + r;
+          if (row < l.M && n < l.N) linear_finish(l, a.row_scales, row, n, GATED ? g[i] : f, f);
+        }
+        __syncwarp();
       }
       tc_fence_before();
       __syncwarp();
@@ -329,14 +375,68 @@ __global__ void __launch_bounds__(256) linear_sum_kernel(const __grid_constant__
   pdl_wait();
   pdl_trigger();
   const LinearArgs& l = a.l;
-  const size_t n = (size_t)l.M * l.N, parts = l.W[1] ? 2 : 1;
+  const int quads = a.np / 4, parts = l.W[1] ? 2 : 1;
+  const size_t n = (size_t)l.M * quads;
   for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (size_t)gridDim.x * blockDim.x) {
-    float v = 0.f, u = 0.f;
+    const int m = (int)(i / quads), c = (int)(i - (size_t)m * quads) * 4;
+    float v[4] = {}, u[4] = {};
     for (int s = 0; s < a.splits; ++s) {
-      v += a.partial[s * parts * n + i];
-      if (parts == 2) u += a.partial[(s * parts + 1) * n + i];
+      const float4 p = *reinterpret_cast<const float4*>(a.partial + ((size_t)s * parts * l.M + m) * a.np + c);
+      v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
+      if (parts == 2) {
+        const float4 q = *reinterpret_cast<const float4*>(a.partial + (((size_t)s * 2 + 1) * l.M + m) * a.np + c);
+        u[0] += q.x, u[1] += q.y, u[2] += q.z, u[3] += q.w;
+      }
     }
-    linear_finish(l, a.row_scales, (int)(i / l.N), (int)(i % l.N), v, u);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (c + j < l.N) linear_finish(l, a.row_scales, m, c + j, v[j], u[j]);
+  }
+}
+
+// x = h + m + l in bf16: h and m rounded to nearest, so that each rest has 8 significant bits
+// less, exactly.  An infinity or NaN is its own h; a finite value that would round to infinity
+// is cut instead.
+__device__ __forceinline__ void split3(float x, uint16_t (&p)[3]) {
+  p[0] = f32_to_bf16(x);
+  if (isinf(bf16_to_f32(p[0])) && isfinite(x)) p[0] = (uint16_t)(__float_as_uint(x) >> 16);
+  float r = x - bf16_to_f32(p[0]);
+  if (!isfinite(r)) r = 0.f;
+  p[1] = f32_to_bf16(r);
+  p[2] = f32_to_bf16(r - bf16_to_f32(p[1]));
+}
+
+// One value per step of each row to its three parts, [3][rows][pitch], zero between cols and
+// pitch.  WF: fp32, or int4 codes times their block scales in fp32.
+template <int WF>
+__global__ void __launch_bounds__(256) linear_split_kernel(const void* __restrict__ W, const float* __restrict__ s, long long ld,
+                                                           int rows, int cols, int pitch, uint16_t* __restrict__ out) {
+  pdl_wait();
+  pdl_trigger();
+  const int quads = pitch / 4;
+  const size_t n = (size_t)rows * quads, plane = (size_t)rows * pitch;
+  for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (size_t)gridDim.x * blockDim.x) {
+    const int r = (int)(i / quads), c = (int)(i - (size_t)r * quads) * 4;
+    float v[4] = {};
+    if (c < cols) {  // cols is a multiple of 4
+      if constexpr (WF == MOE_W_F32) {
+        const float4 f = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(W) + (size_t)r * ld + c));
+        v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+      } else {
+        constexpr int kShift = WF == MOE_W_INT4_B32 ? 5 : 7;
+        const uint32_t q = __ldg(reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(W) + ((size_t)r * cols + c) / 2));
+        const float scale = __ldg(s + (size_t)r * (cols >> kShift) + (c >> kShift));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = (float)((int)(q << (28 - 4 * j)) >> 28) * scale;
+      }
+    }
+    uint16_t p[4][3];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) split3(v[j], p[j]);
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      *reinterpret_cast<uint2*>(out + k * plane + (size_t)r * pitch + c) =
+          make_uint2(p[0][k] | (uint32_t)p[1][k] << 16, p[2][k] | (uint32_t)p[3][k] << 16);
   }
 }
 
@@ -375,44 +475,72 @@ __global__ void __launch_bounds__(256) linear_widen_kernel(const void* __restric
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
+// fp32: at most this many 64-column steps of a product in one accumulator.  The tensor core
+// cuts its sums off, which pulls them towards zero by up to 2^-24 of the sum a step.
+constexpr int kF32Steps = 12;
+
 struct TcLayout {
-  int mt, nt, ksteps, splits;
-  size_t w[2], partial, total;  // offsets in the workspace
+  int mt, nt, ksteps, splits, pitch, np;
+  int xparts, wparts;
+  bool w_copy;                // the weights are read from the workspace
+  size_t x, w[2], partial, total;  // offsets in the workspace
 };
 TcLayout tc_layout(const moe_linear_desc& d, int M) {
   TcLayout t;
-  const bool gated = d.W_up != nullptr;
-  const int outs = gated ? kRows : 2 * kRows;
+  const bool gated = d.W_up != nullptr, int4 = d.wfmt == MOE_W_INT4_B32 || d.wfmt == MOE_W_INT4_B128;
+  const bool f32 = d.xfmt == MOE_X_F32 || d.wfmt == MOE_W_F32;
+  const int outs = gated ? kRows : 2 * kRows, sides = gated ? 2 : 1;
+  t.xparts = d.xfmt == MOE_X_F32 ? 3 : 1;
+  t.wparts = d.wfmt == MOE_W_F32 || (int4 && d.xfmt == MOE_X_F32) ? 3 : 1;
   t.mt = (M + 2 * kRows - 1) / (2 * kRows);
   t.nt = (d.N + outs - 1) / outs;
   t.ksteps = (d.K + kK - 1) / kK;
+  t.pitch = (d.K + 7) / 8 * 8;
+  t.np = (d.N + 15) / 16 * 16;
   // 74 pairs of SMs: split the reduction while the tiles leave half of them idle and a part
   // keeps 8 stages (the pipeline's fill) to work on
+  const int steps = t.ksteps * (t.xparts == 1 ? t.wparts : (t.wparts == 1 ? t.xparts : 6));
   t.splits = 1;
-  while ((long long)t.mt * t.nt * t.splits * 2 <= 74 && t.ksteps >= 16 * t.splits) t.splits *= 2;
-  const size_t wide = d.wfmt == MOE_W_BF16 ? 0 : up256((size_t)d.N * d.K * 2);
+  while ((long long)t.mt * t.nt * t.splits * 2 <= 74 && steps >= 16 * t.splits && t.ksteps >= 2 * t.splits) t.splits *= 2;
+  if (f32) t.splits = std::max(t.splits, (t.ksteps + kF32Steps - 1) / kF32Steps);
+  t.w_copy = d.wfmt != MOE_W_BF16;
+  const size_t wide = t.w_copy ? up256((size_t)t.wparts * d.N * t.pitch * 2) : 0;
   t.w[0] = 0;
   t.w[1] = wide;
-  t.partial = wide * (gated ? 2 : 1);
-  t.total = t.partial + (t.splits > 1 ? (size_t)t.splits * (gated ? 2 : 1) * M * d.N * 4 : 0);
+  t.x = wide * sides;
+  t.partial = t.x + (t.xparts == 3 ? up256((size_t)3 * M * t.pitch * 2) : 0);
+  t.total = t.partial + (t.splits > 1 ? (size_t)t.splits * sides * M * t.np * 4 : 0);
   return t;
 }
 
 }  // namespace
 
 bool linear_tc_ok(const moe_linear_desc& d, int M) {
-  return d.xfmt == MOE_X_BF16 && d.wfmt != MOE_W_F32 && M > kLinearStreamTokens;
+  const bool f32 = d.xfmt == MOE_X_F32 || d.wfmt == MOE_W_F32;
+  return M > (f32 ? kLinearRowTokens : kLinearStreamTokens);
 }
 
 size_t linear_tc_workspace(const moe_linear_desc& d, int M) { return tc_layout(d, M).total; }
+
+static dim3 grid_for(size_t items, int num_sms) {
+  return dim3((unsigned)std::min<size_t>((items + 255) / 256, (size_t)num_sms * 8));
+}
 
 cudaError_t launch_linear_widen(const moe_linear_desc& d, int M, int which, void* workspace, int num_sms, cudaStream_t s) {
   const TcLayout t = tc_layout(d, M);
   const void* W = which ? d.W_up : d.W;
   const float* sc = which ? d.s_up : d.s;
   uint16_t* out = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + t.w[which]);
+  const dim3 block(256);
+  if (t.wparts == 3) {
+    const dim3 grid = grid_for((size_t)d.N * t.pitch / 4, num_sms);
+    auto go = [&](auto kernel) { return launch_k(kernel, grid, block, 0, s, W, sc, (long long)d.K, d.N, d.K, t.pitch, out); };
+    return d.wfmt == MOE_W_F32 ? go(linear_split_kernel<MOE_W_F32>)
+                               : (d.wfmt == MOE_W_INT4_B32 ? go(linear_split_kernel<MOE_W_INT4_B32>)
+                                                           : go(linear_split_kernel<MOE_W_INT4_B128>));
+  }
   const size_t n16 = (size_t)d.N * d.K / 16;
-  const dim3 grid((unsigned)std::min<size_t>((n16 + 255) / 256, (size_t)num_sms * 8)), block(256);
+  const dim3 grid = grid_for(n16, num_sms);
   switch (d.wfmt) {
     case MOE_W_INT8_ROW: return launch_k(linear_widen_kernel<MOE_W_INT8_ROW>, grid, block, 0, s, W, sc, n16, d.K, out);
     case MOE_W_INT4_B32: return launch_k(linear_widen_kernel<MOE_W_INT4_B32>, grid, block, 0, s, W, sc, n16, d.K, out);
@@ -420,11 +548,19 @@ cudaError_t launch_linear_widen(const moe_linear_desc& d, int M, int which, void
   }
 }
 
+cudaError_t launch_linear_split_x(const moe_linear_desc& d, const LinearArgs& a, void* workspace, int num_sms, cudaStream_t s) {
+  const TcLayout t = tc_layout(d, a.M);
+  return launch_k(linear_split_kernel<MOE_W_F32>, grid_for((size_t)a.M * t.pitch / 4, num_sms), dim3(256), 0, s, a.x,
+                  static_cast<const float*>(nullptr), a.ldx, a.M, d.K, t.pitch,
+                  reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + t.x));
+}
+
 static TcArgs tc_args(const moe_linear_desc& d, const LinearArgs& a, const TcLayout& t, void* workspace) {
   TcArgs p = {};
   p.l = a;
   p.row_scales = d.wfmt == MOE_W_INT8_ROW;
   p.mt = t.mt, p.nt = t.nt, p.splits = t.splits, p.ksteps = t.ksteps;
+  p.xparts = t.xparts, p.wparts = t.wparts, p.np = t.np;
   const int yb = d.yfmt == MOE_X_F32 ? 4 : 2;
   auto pieces = [&](const void* q, long long ld) { return reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld * yb % 16 == 0; };
   p.vec = pieces(a.y, a.ldy) && (!a.residual || pieces(a.residual, a.ldr));
@@ -437,14 +573,15 @@ cudaError_t launch_linear_tc(const moe_linear_desc& d, const LinearArgs& a, void
   const TcLayout t = tc_layout(d, a.M);
   const TcArgs p = tc_args(d, a, t, workspace);
   const bool gated = d.W_up != nullptr;
+  char* ws = static_cast<char*>(workspace);
   CUtensorMap mx, mw[2];
-  cudaError_t e = make_tmap(&mx, a.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (uint64_t)d.K, (uint64_t)a.M, (uint64_t)a.ldx * 2, kK,
-                            kRows, CU_TENSOR_MAP_SWIZZLE_128B);
-  for (int i = 0; i < (gated ? 2 : 1) && e == cudaSuccess; ++i) {
-    const void* W = d.wfmt == MOE_W_BF16 ? a.W[i] : static_cast<char*>(workspace) + t.w[i];
-    e = make_tmap(&mw[i], W, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (uint64_t)d.K, (uint64_t)d.N, (uint64_t)d.K * 2, kK, kRows,
+  const void* x = t.xparts == 3 ? ws + t.x : a.x;
+  cudaError_t e = make_tmap(&mx, x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (uint64_t)d.K, (uint64_t)a.M * t.xparts,
+                            t.xparts == 3 ? (uint64_t)t.pitch * 2 : (uint64_t)a.ldx * 2, kK, kRows, CU_TENSOR_MAP_SWIZZLE_128B);
+  for (int i = 0; i < (gated ? 2 : 1) && e == cudaSuccess; ++i)
+    e = make_tmap(&mw[i], t.w_copy ? ws + t.w[i] : a.W[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (uint64_t)d.K,
+                  (uint64_t)d.N * t.wparts, t.wparts == 3 ? (uint64_t)t.pitch * 2 : (uint64_t)d.K * 2, kK, kRows,
                   CU_TENSOR_MAP_SWIZZLE_128B);
-  }
   if (!gated) mw[1] = mw[0];
   auto kernel = gated ? linear_tc_kernel<true> : linear_tc_kernel<false>;
   static std::atomic<bool> allowed[2][64];
@@ -458,9 +595,8 @@ cudaError_t launch_linear_tc(const moe_linear_desc& d, const LinearArgs& a, void
 bool linear_tc_split(const moe_linear_desc& d, int M) { return tc_layout(d, M).splits > 1; }
 
 cudaError_t launch_linear_sum(const moe_linear_desc& d, const LinearArgs& a, void* workspace, int num_sms, cudaStream_t s) {
-  const TcArgs p = tc_args(d, a, tc_layout(d, a.M), workspace);
-  const size_t n = (size_t)a.M * a.N;
-  return launch_k(linear_sum_kernel, dim3((unsigned)std::min<size_t>((n + 255) / 256, (size_t)num_sms * 8)), dim3(256), 0, s, p);
+  const TcLayout t = tc_layout(d, a.M);
+  return launch_k(linear_sum_kernel, grid_for((size_t)a.M * t.np / 4, num_sms), dim3(256), 0, s, tc_args(d, a, t, workspace));
 }
 
 }  // namespace moe
