@@ -60,7 +60,8 @@ __global__ void __launch_bounds__(kRouterThreads)
   constexpr int kSums = kRouterExperts * TT, kRWarps = kRouterThreads / 32;
   __shared__ double part[kRWarps][kSums];
   const int e0 = blockIdx.x * kRouterExperts, tid = threadIdx.x, w = warp_id(), lane = lane_id();
-  if (blockIdx.x == 0 && tid < kFewCounters) counters[tid] = 0;
+  if (blockIdx.x == 0)
+    for (int i = tid; i < kFewCounters; i += kRouterThreads) counters[i] = 0;
   const float* row[kRouterExperts];
 #pragma unroll
   for (int i = 0; i < kRouterExperts; ++i) row[i] = W_r + (size_t)min(e0 + i, E - 1) * H;
@@ -384,7 +385,11 @@ __global__ void __launch_bounds__(kFewThreads) few_layer_kernel(const FewArgs a)
 // memory; the warp whose share of the unit is smallest adds them up, applies the activation
 // and stores h.  (One copying, one summing and ten multiplying warps measured worse: the
 // summing warp, all latency, held up the rest.)
-// After a barrier over the grid a CTA computes 16 rows of y for every chosen expert (and the
+// Units are dealt out as lists, one per CTA.  Nothing makes the CTAs of a launch run at the same
+// time (another launch of this kind may hold SMs and wait as well), so a CTA that is done
+// with its list takes over those that no CTA has started on, and one that starts late and
+// finds its list taken leaves: whoever waits at the barrier waits for CTAs that are running.
+// After that barrier over the lists a CTA computes 16 rows of y for every chosen expert (and the
 // shared one), one after the other, so the combine stays inside the CTA.  Down weights do not
 // depend on h: the rings are full of them before the barrier opens.  h is handed over as
 // bf16 value plus bf16 remainder (16 significant bits): the remainder takes token columns of
@@ -427,6 +432,9 @@ struct StreamShared {
   uint64_t full[kWarps][kMaxStages];
   uint64_t rfull[kWarps][2], rempty[kWarps][2];  // by team: its warps' sums of a unit written / added up
   int n_up, n_down;              // entries
+  int adopted;                   // a list taken over, -1 for none
+  int taken, all;                // this CTA's list is another's; every CTA has started
+  uint16_t lists[kFewLists];     // this CTA's lists
   float pair_w[kMaxPairs];
   uint16_t pair[kMaxPairs];      // valid pairs in expert order: pair | token << 9
   uint32_t up[kMaxPairs + 2], down[kMaxPairs + 4];  // entries: shared first / shared last
@@ -492,6 +500,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   __syncthreads();
   pdl_wait();
   pdl_trigger();
+  if (threadIdx.x == 0) {
+    atomicAdd(&a.counters[0], 1u);
+    sh.taken = atomicExch(&a.counters[kFewOwner + blockIdx.x], 1u) != 0;
+  }
 
   const int P = a.T * a.k, grid = (int)gridDim.x;
   const int su = a.Is ? (a.T + kUpTokens - 1) / kUpTokens : 0, sd = a.Is ? (a.T + kDownTokens - 1) / kDownTokens : 0;
@@ -518,8 +530,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     k.block += grid * up_teams;
     for (int of; k.block >= (of = k.entry < su ? sb : ub); ++k.entry) k.block -= of;
   };
-  auto first_unit = [&](int j) {
-    UpWalk k = {-1, 0, ((int)blockIdx.x - grid) * up_teams + up_team, j};
+  auto first_unit = [&](int list, int j) {
+    UpWalk k = {-1, 0, (list - grid) * up_teams + up_team, j};
     step_unit(k);
     return k;
   };
@@ -545,15 +557,15 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       k.x += down_teams;
     }
   };
-  auto first_down = [&] {
-    DownWalk k = {(int)blockIdx.x - grid, n_down, 0};
+  auto first_down = [&](int list) {
+    DownWalk k = {list - grid, n_down, 0};
     seek_down(k);
     return k;
   };
 
   // copies run kStages ahead: `head` and `head_down` are the next to start
   int issued = 0, in_slot = 0;
-  UpWalk head = first_unit(up_w);
+  UpWalk head = first_unit((int)blockIdx.x, up_w);
   seek_up(head);
   DownWalk head_down = {hb, 0, 0};
   auto issue = [&](bool down) {
@@ -645,12 +657,21 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     const int n = list_entries(sh, P, kDownTokens, sh.down, 0);
     if (lane < sd) sh.down[n + lane] = pack_entry(kSharedEntry, lane * kDownTokens, min(kDownTokens, a.T - lane * kDownTokens));
     if (lane == 0) sh.n_down = n + sd;
+  } else if (w == 2 && lane == 0) {
+    sh.all = *reinterpret_cast<volatile uint32_t*>(&a.counters[0]) >= (uint32_t)grid;
   }
   __syncthreads();
   n_up = sh.n_up;
   n_down = sh.n_down;
-  head_down = first_down();
-  for (int i = issued; i < R::kStages; ++i) issue_next();
+  // the usual case: every CTA has started, so no list will be left over, and the rings may run on
+  // into the down weights
+  const bool all = sh.all != 0;
+  if (all) head_down = first_down((int)blockIdx.x);
+  auto fill = [&](int have) {
+#pragma unroll 1
+    for (int i = have; i < R::kStages; ++i) issue_next();
+  };
+  if (!sh.taken) fill(issued);
   // this warp's tokens' experts, for the weights later; then the plan's space becomes the units' sums
   int my_e[2] = {-1, -1};
 #pragma unroll
@@ -675,12 +696,13 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   };
 
   // ---------------------------------------------------------------- gate and up
-  {
+  int n_lists = 0, events = 0;
+  for (int list = sh.taken ? -1 : (int)blockIdx.x; list >= 0;) {
     float acc[2][4] = {};
-    UpWalk unit = first_unit(0);  // the next to hand over
+    UpWalk unit = first_unit(list, 0);  // the next to hand over
     // this warp's sums of the unit to shared memory; the warp whose turn it is adds them up
     auto hand_over = [&] {
-      const int buf = unit.n & 1, parity = (unit.n >> 1) & 1;
+      const int buf = events & 1, parity = (events >> 1) & 1;
       const int from = a.team == 1 ? 0 : unit.n * boxes_h % a.team;  // the warps that had boxes, in their order
       const int shares = min(boxes_h, a.team);
       few_wait(&sh.rempty[up_team][buf], parity ^ 1, dead, a.flags);
@@ -738,9 +760,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           at[a.plane] = isfinite(rest) ? f32_to_bf16(rest) : (uint16_t)0;
         }
       }
+      ++events;
       step_unit(unit);
     };
-    UpWalk at = first_unit(up_w);
+    UpWalk at = first_unit(list, up_w);
     seek_up(at);
     uint4 x[F::kLoads], x_next[F::kLoads];
     const uint16_t* tok = nullptr;  // the lane's token, of the unit at `at`
@@ -758,8 +781,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       fetch();
     }
 #pragma unroll 1
-    while (at.entry < n_up) {
-      while (unit.n < at.n) hand_over();
+    for (;;) {
+      const bool more = at.entry < n_up;
+      while (more ? unit.n < at.n : unit.entry < n_up) hand_over();
+      if (!more) break;
 #pragma unroll
       for (int i = 0; i < F::kLoads; ++i) x[i] = x_next[i];
       const uint32_t stage = smem_u32(ring + out_slot * R::kStage);
@@ -786,24 +811,53 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       stream::mac_box<WF, 2>(stage, x, sc, acc);
       read();
     }
-    while (unit.entry < n_up) hand_over();
+    if (threadIdx.x == 0) sh.lists[n_lists] = (uint16_t)list;
+    ++n_lists;
+    list = -1;
+    if (!all) {
+      if (threadIdx.x == 0) {
+        int b = 0;
+        while (b < grid && (*reinterpret_cast<volatile uint32_t*>(&a.counters[kFewOwner + b]) != 0 ||
+                            atomicExch(&a.counters[kFewOwner + b], 1u) != 0))
+          ++b;
+        sh.adopted = b < grid ? b : -1;
+      }
+      __syncthreads();
+      list = sh.adopted;
+      __syncthreads();
+      if (list >= 0) {
+        head = first_unit(list, up_w);
+        seek_up(head);
+        fill(0);
+      }
+    }
   }
   // the weights, while the grid finishes; the down units need them
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int t = w + i * kWarps;
-    if (t >= a.T) break;
+    if (t >= a.T || n_lists == 0) break;
     const float wt = few_weight(a, t, my_e[i]);
     if (lane < a.k) sh.pair_w[t * a.k + lane] = wt;
-    if (blockIdx.x == 0) few_write_route(a, t, my_e[i], wt);
+    bool first = blockIdx.x == 0;  // the owner of the first list writes the routing out
+    for (int j = 1; j < n_lists; ++j) first |= sh.lists[j] == 0;
+    if (first) few_write_route(a, t, my_e[i], wt);
   }
 
   // ---------------------------------------------------------------- every h is stored
   __syncthreads();
+  if (n_lists == 0) {
+    // taken over: the copies that were started have to land first
+    for (; done < issued; ++done) {
+      mbar_wait(&sh.full[w][out_slot], phase);
+      if (++out_slot == R::kStages) out_slot = 0, phase ^= 1u;
+    }
+    return;
+  }
   for (int i = threadIdx.x; i < kWarps * MOE_FEW_MAX_TOKENS * 16; i += kStreamThreads) (&sh.y[0][0][0])[i] = 0.f;
   if (threadIdx.x == 0) {
     __threadfence();
-    atomicAdd(&a.counters[kFewDone], 1u);
+    atomicAdd(&a.counters[kFewDone], (uint32_t)n_lists);
     const uint64_t t0 = global_timer_ns();
     for (;;) {
       uint32_t v;
@@ -822,7 +876,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   // ---------------------------------------------------------------- down and combine
   constexpr int DB = R::kDownBoxes;
   uint4 x_next[DB][F::kLoads];
-  DownWalk at = first_down();
+  DownWalk at;
   // of the entry at `at`: its tokens, reduction length, the lane's token (value or remainder)
   uint32_t en = 0;
   int K = 0;
@@ -846,11 +900,18 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       if (d == 0 || left > d * F::kBoxCols)
         stream::load_token<WF>(tok + c0 + d * F::kBoxCols, left - d * F::kBoxCols, x_next[d]);
   };
+#pragma unroll 1
+  for (int i = 0; i < n_lists; ++i) {
+  at = first_down(sh.lists[i]);
+  if (!all || i > 0) {
+    head_down = at;
+    fill(0);
+  }
   if (at.blk < hb) {
     entry_of();
     fetch();
   }
-  for (int blk = (int)blockIdx.x; blk < hb; blk += grid) {
+  for (int blk = sh.lists[i]; blk < hb; blk += grid) {
     float acc[1][4] = {};
 #pragma unroll 1
     while (at.blk == blk) {
@@ -925,6 +986,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     }
     __syncthreads();
   }
+  }
   // after a wait that ran out: leave only when the copies have landed
   if (dead) {
     for (; done < issued; ++done) {
@@ -983,8 +1045,7 @@ cudaError_t launch_stream(FewArgs a, int num_sms, cudaStream_t s) {
   static std::atomic<bool> allowed[64];
   if (e == cudaSuccess) e = allow_smem(reinterpret_cast<const void*>(few_stream_kernel<WF>), smem, allowed);
   if (e != cudaSuccess) return e;
-  // cooperative: the grid's barrier needs every CTA resident (one per SM)
-  return launch_k_cooperative(few_stream_kernel<WF>, dim3(num_sms), dim3(kStreamThreads), smem, s, m, a);
+  return launch_k_after(few_stream_kernel<WF>, dim3(std::min(num_sms, kFewLists)), dim3(kStreamThreads), smem, s, m, a);
 }
 
 // The scales of a [rows, K] int4 block-32 matrix can be copied by TMA: rows of whole 16-byte
@@ -998,8 +1059,8 @@ cudaError_t launch_layer(const moe_desc& d, const FewArgs& a, int num_sms, cudaS
   if constexpr (WF != MOE_W_F32)
     if (d.xfmt == MOE_X_BF16) return launch_stream<WF>(a, num_sms, s);
   const dim3 grid(num_sms * 4), block(kFewThreads);
-  if (d.xfmt == MOE_X_F32) return launch_k(few_layer_kernel<WF, MOE_X_F32>, grid, block, 0, s, a);
-  if constexpr (WF == MOE_W_F32) return launch_k(few_layer_kernel<WF, MOE_X_BF16>, grid, block, 0, s, a);
+  if (d.xfmt == MOE_X_F32) return launch_k_after(few_layer_kernel<WF, MOE_X_F32>, grid, block, 0, s, a);
+  if constexpr (WF == MOE_W_F32) return launch_k_after(few_layer_kernel<WF, MOE_X_BF16>, grid, block, 0, s, a);
   return cudaErrorInvalidValue;  // not reached
 }
 

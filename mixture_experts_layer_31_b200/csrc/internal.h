@@ -37,19 +37,18 @@ cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sme
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Launch of a kernel whose CTAs wait for one another: cooperative, so that it starts only when
-// all of them fit on the GPU beside what already runs.
+// The same for the second of two launches that belong together: it may always start while the
+// first, which triggers it, is finishing.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_k_cooperative(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
-                                 Args&&... args) {
+cudaError_t launch_k_after(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeCooperative;
-  attr[0].val.cooperative = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
@@ -206,10 +205,12 @@ cudaError_t launch_expert_counts(const int32_t* idx, int64_t n, int E, uint64_t*
 cudaError_t launch_combine(const moe_desc& d, const int32_t* idx, int T, const void* yp, bool yp_bf16, void* y,
                            cudaStream_t s, const float* ys = nullptr, const void* residual = nullptr);
 // ---- the layer for a few tokens (two launches) ----
-// counters at the start of its workspace: [0] claimed units, [kFewDone] finished gate/up
-// units, each in a 128-byte line of its own
-constexpr int kFewCounters = 64;
+// counters at the start of its workspace: [0] claimed units or started CTAs, [kFewDone] finished
+// gate/up units or lists, each in a 128-byte line of its own, then the lists' owners
 constexpr int kFewDone = 32;
+constexpr int kFewOwner = 64;
+constexpr int kFewLists = 256;
+constexpr int kFewCounters = kFewOwner + kFewLists;
 size_t few_workspace_bytes(const moe_desc& d, const moe_shared_expert* sh, int T);
 cudaError_t launch_few_router(const moe_desc& d, const moe_shared_expert* sh, const void* x, int T, void* workspace,
                               uint32_t* flags, cudaStream_t s);

@@ -18,8 +18,13 @@ struct LinearArgs {
   long long ldy;
 };
 
-// up to this many tokens the weights stream through warp-wide matrix instructions
-constexpr int kLinearStreamTokens = 64;
+// Up to this many bf16 tokens the weights stream through warp-wide matrix instructions; beyond, the
+// tensor cores take them, quantised ones after a pass that widens them.  Measured, stream and
+// tensor cores: bf16 9216 x 2304, 32 tokens 23 and 22 us, 64 tokens 42 and 25; int8, the same
+// shape, 64 tokens 36 and 42; int4 2048 x 4999, 17 tokens 25 and 25, 32 tokens 31 and 26.
+inline int linear_stream_tokens(int wfmt) {
+  return wfmt == MOE_W_BF16 ? 32 : (wfmt == MOE_W_INT8_ROW ? 64 : 16);
+}
 
 __device__ __forceinline__ float linear_act(float v, int act) {
   if (act == MOE_ACT_SILU) return silu_mul(v, 1.f);

@@ -230,7 +230,7 @@ cudaError_t launch(const moe_linear_desc& d, const LinearArgs& a, int num_sms, u
 }  // namespace
 
 bool linear_stream_ok(const moe_linear_desc& d, int M) {
-  return d.xfmt == MOE_X_BF16 && d.wfmt != MOE_W_F32 && M <= kLinearStreamTokens;
+  return d.xfmt == MOE_X_BF16 && d.wfmt != MOE_W_F32 && M <= linear_stream_tokens(d.wfmt);
 }
 
 cudaError_t launch_linear_stream(const moe_linear_desc& d, const LinearArgs& a, int num_sms, uint32_t* flags, cudaStream_t s) {

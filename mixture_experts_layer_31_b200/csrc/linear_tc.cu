@@ -20,9 +20,12 @@
 // significant bits each, exactly: the products of parts that matter to 24 bits (six of two
 // fp32 operands, three where one is exact in bf16) are summed, the small ones first; what is
 // left out is below 2^-23 of each product.  That is six times the operations of a bf16
-// product and still several times the rate of fp32 multiply-adds.  The tensor core's own
-// additions round towards zero, so long reductions are split and the parts' sums added in
-// fp32 (kF32Steps).
+// product and still several times the rate of fp32 multiply-adds.
+// The tensor core's own additions cut off: over 2,304 columns in one accumulator the result
+// came out 2 x 10^-6 too small (of its mean magnitude), over 9,216 columns 4 x 10^-6.  Where the
+// output is fp32, the accumulator is therefore drained every kSegment stages and the drained
+// sums are added in fp32 registers, rounded to nearest: 7 x 10^-7 off, as a chain of fp32
+// multiply-adds is.  A bf16 output's own rounding is a thousand times that.
 // Quantised weights are widened to bf16 in the workspace first: int8 codes exactly, with the row
 // scale left for the epilogue, int4 as q s rounded once (half a step of bf16 per weight, as the
 // routed layer's tensor-core path has it; the relative error of a sum is below y's own rounding).
@@ -55,7 +58,7 @@ struct TcArgs {
   LinearArgs l;
   int row_scales;       // int8: the epilogue scales the sums
   int mt, nt, splits;   // tiles of 256 tokens, of 256 (gated: 128) outputs; parts of the reduction
-  int ksteps;
+  int ksteps, segment;  // columns steps of the reduction; of one accumulator
   int xparts, wparts;   // bf16 parts of x and of W: 1, or 3 of an fp32 operand (its rows follow one another)
   int vec;              // y and residual rows in 16-byte pieces
   float* partial;       // splits > 1: [splits][1 or 2][M][np]
@@ -130,7 +133,23 @@ __device__ __forceinline__ Tile tile_of(const TcArgs& a, int t) {
   return r;
 }
 
-// 16 outputs of token m from column n0 on
+// The epilogue's code is kept short on purpose: a tile passes through it once, and its way into the
+// instruction cache shows (with every activation inlined for every column it took 17 us before
+// the first tile was stored, whatever the reduction's length).
+
+// the activation of 16 sums: v / (1 + exp(-z)), z = v (SiLU) or twice the tanh-GELU's argument
+template <bool FAST>
+__device__ __forceinline__ void activate16(float (&v)[16], int act) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const float z = act == MOE_ACT_SILU ? v[j] : 2.0f * gelu_tanh_z(v[j]);
+    // FAST, for bf16 outputs: a few units in the last place of fp32
+    if (FAST) v[j] = __fdividef(v[j], 1.0f + __expf(fminf(-z, 80.0f)));
+    else v[j] = v[j] / (1.0f + expf(-z));
+  }
+}
+
+// 16 outputs of token m from column n0 on, in 16-byte pieces
 template <bool GATED>
 __device__ __forceinline__ void finish16(const TcArgs& a, int split, int m, int n0, const uint32_t (&v)[16],
                                          const uint32_t (&u)[16]) {
@@ -145,23 +164,34 @@ __device__ __forceinline__ void finish16(const TcArgs& a, int split, int m, int 
     }
     return;
   }
-  float y[16];
+  float y[16], g[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
-    float s = __uint_as_float(v[j]);
-    if (a.row_scales) s *= __ldg(l.s[0] + n0 + j);
-    if (l.b[0]) s += __ldg(l.b[0] + n0 + j);
-    // outputs in bf16: the fast forms, a few units in the last place of fp32
-    const bool fast = l.yfmt == MOE_X_BF16;
-    if (l.act == MOE_ACT_SILU) s = fast ? silu_mul_fast(s, 1.f) : silu_mul(s, 1.f);
-    if (l.act == MOE_ACT_GELU_TANH) s = fast ? gelu_tanh_mul_fast(s, 1.f) : gelu_tanh_mul(s, 1.f);
-    if (GATED) {
-      float g = __uint_as_float(u[j]);
-      if (a.row_scales) g *= __ldg(l.s[1] + n0 + j);
-      if (l.b[1]) g += __ldg(l.b[1] + n0 + j);
-      s *= g;
+    y[j] = __uint_as_float(v[j]);
+    if (GATED) g[j] = __uint_as_float(u[j]);
+  }
+  if (a.row_scales) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      y[j] *= __ldg(l.s[0] + n0 + j);
+      if (GATED) g[j] *= __ldg(l.s[1] + n0 + j);
     }
-    y[j] = s;
+  }
+  if (l.b[0]) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) y[j] += __ldg(l.b[0] + n0 + j);
+  }
+  if (l.act != MOE_ACT_NONE) {
+    if (l.yfmt == MOE_X_BF16) activate16<true>(y, l.act);
+    else activate16<false>(y, l.act);
+  }
+  if constexpr (GATED) {
+    if (l.b[1]) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) g[j] += __ldg(l.b[1] + n0 + j);
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) y[j] *= g[j];
   }
   if (l.yfmt == MOE_X_BF16) {
     uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(l.y) + (size_t)m * l.ldy + n0);
@@ -195,7 +225,43 @@ __device__ __forceinline__ void finish16(const TcArgs& a, int split, int m, int 
   }
 }
 
+// 16 columns of the warp's 32 tokens, the lane's token m; the whole warp calls it
 template <bool GATED>
+__device__ __forceinline__ void output16(const TcArgs& a, int split, int m, int n0, const uint32_t (&v)[16],
+                                         const uint32_t (&u)[16], float* turn) {
+  const LinearArgs& l = a.l;
+  if (a.splits > 1 || (a.vec && n0 + 16 <= l.N)) {
+    if (m < l.M) finish16<GATED>(a, split, m, n0, v, u);
+    return;
+  }
+  // rows of y that 16-byte pieces do not fit: turned from a row a lane to some rows at a time, 16
+  // columns each (gated: 8, with their up sums beside them)
+  constexpr int kWide = GATED ? 8 : 16;
+  const int lane = lane_id();
+#pragma unroll
+  for (int p = 0; p < 16 / kWide; ++p) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      turn[lane * 17 + j] = __uint_as_float(!GATED ? v[j] : (j < 8 ? v[(8 * p + j) & 15] : u[(8 * p + j - 8) & 15]));
+    __syncwarp();
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32; r0 += 32 / kWide) {
+      const int r = r0 + lane / kWide, c = lane % kWide, row = m - lane + r, n = n0 + p * kWide + c;
+      if (row < l.M && n < l.N) linear_finish(l, a.row_scales, row, n, turn[r * 17 + c], turn[r * 17 + (GATED ? 8 + c : c)]);
+    }
+    __syncwarp();
+  }
+}
+// one copy of it for a loop that is unrolled: eight copies' way into the instruction cache took
+// longer than all the rest (37 us a tile)
+template <bool GATED>
+__device__ __noinline__ void output16_call(const TcArgs& a, int split, int m, int n0, const uint32_t (&v)[16],
+                                           const uint32_t (&u)[16], float* turn) {
+  output16<GATED>(a, split, m, n0, v, u, turn);
+}
+
+// SEG: the reduction goes through the accumulators in segments
+template <bool GATED, bool SEG>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     linear_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w0,
                      const __grid_constant__ CUtensorMap map_w1, const __grid_constant__ TcArgs a, uint32_t* flags) {
@@ -255,9 +321,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const Tile tl = tile_of(a, t);
         int k0;
         const int nk = steps_of(tl.split, k0), all = nk * products(a.xparts, a.wparts);
+        const int seg = SEG ? a.segment : nk;
         const int row_x = tl.m * 2 * kRows + (int)rank * kRows;
         const int row_w = GATED ? tl.n * kRows : tl.n * 2 * kRows + (int)rank * kRows;
-        int k = 0, i = 0;
+        // segment by segment the products of parts, each over the segment's columns
+        int k = 0, i = 0, from = 0, to = min(seg, nk);
         Parts p = product(a.xparts, a.wparts, 0);
         for (int n = 0; n < all; ++n, ++it) {
           const int s = it % kStages;
@@ -269,7 +337,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           // a tile's last rows may be the next part's first: rows past M and N are not used
           tma_load_pair(stage, &map_x, (k0 + k) * kK, row_x + p.x * a.l.M, bar);
           tma_load_pair(stage + kHalf, map_w, (k0 + k) * kK, row_w + p.w * a.l.N, bar);
-          if (++k == nk) k = 0, p = product(a.xparts, a.wparts, ++i);
+          if (++k == to) {
+            if (++i == products(a.xparts, a.wparts)) i = 0, from = to, to = min(to + seg, nk);
+            k = from;
+            p = product(a.xparts, a.wparts, i);
+          }
         }
       }
       // after a wait that ran out: the copies in flight end before the pair leaves
@@ -281,25 +353,28 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       bool dead = false;
       uint32_t it = 0, n = 0;
       const uint32_t idesc = umma_idesc_bf16(2 * kRows, kTileN);
-      for (int t = pair; t < tiles && !dead; t += pairs, ++n) {
+      for (int t = pair; t < tiles && !dead; t += pairs) {
         const Tile tl = tile_of(a, t);
         int k0;
-        const int nk = steps_of(tl.split, k0) * products(a.xparts, a.wparts);
-        const uint32_t buf = n & 1u, d = tmem + buf * kTileN;
-        wait(&acc_empty[buf], ((n >> 1) & 1u) ^ 1u, dead);
-        tc_fence_after();
-        for (int k = 0; k < nk && !dead; ++k, ++it) {
-          const int s = it % kStages;
-          wait(&full[s], (it / kStages) & 1u, dead);
-          if (dead) break;
+        const int nk = steps_of(tl.split, k0), seg = SEG ? a.segment : nk, prods = products(a.xparts, a.wparts);
+        for (int from = 0; from < nk && !dead; from += seg, ++n) {
+          const int all = min(seg, nk - from) * prods;
+          const uint32_t buf = n & 1u, d = tmem + buf * kTileN;
+          wait(&acc_empty[buf], ((n >> 1) & 1u) ^ 1u, dead);
           tc_fence_after();
-          const uint32_t stage = smem_u32(smem + s * kStage);
+          for (int k = 0; k < all && !dead; ++k, ++it) {
+            const int s = it % kStages;
+            wait(&full[s], (it / kStages) & 1u, dead);
+            if (dead) break;
+            tc_fence_after();
+            const uint32_t stage = smem_u32(smem + s * kStage);
 #pragma unroll
-          for (int j = 0; j < kK / 16; ++j)
-            umma_pair(d, umma_desc_sw128(stage + 32 * j), umma_desc_sw128(stage + kHalf + 32 * j), idesc, (k | j) != 0);
-          commit_pair(&empty[s]);
+            for (int j = 0; j < kK / 16; ++j)
+              umma_pair(d, umma_desc_sw128(stage + 32 * j), umma_desc_sw128(stage + kHalf + 32 * j), idesc, (k | j) != 0);
+            commit_pair(&empty[s]);
+          }
+          if (!dead) commit_pair(&acc_full[buf]);
         }
-        if (!dead) commit_pair(&acc_full[buf]);
       }
     }
   } else if (w >= 4) {
@@ -309,54 +384,71 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const LinearArgs& l = a.l;
     bool dead = false;
     uint32_t n = 0;
-    for (int t = pair; t < tiles; t += pairs, ++n) {
+    for (int t = pair; t < tiles && !dead; t += pairs) {
       const Tile tl = tile_of(a, t);
-      const uint32_t buf = n & 1u;
-      wait(&acc_full[buf], (n >> 1) & 1u, dead);
-      dead = __any_sync(0xFFFFFFFFu, dead);
-      if (dead) break;
-      tc_fence_after();
       const int m = tl.m * 2 * kRows + (int)rank * kRows + q * 32 + lane;
       const int c_first = tl.n * outs + group * kCols;
-      const uint32_t at = tmem + buf * kTileN + ((uint32_t)(q * 32) << 16) + group * kCols;
-#pragma unroll 1
+      const uint32_t column = tmem + ((uint32_t)(q * 32) << 16) + group * kCols;
+      auto drain = [&](uint32_t buf) {  // the accumulator has been read
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(leader_addr(&acc_empty[buf]));
+      };
+      auto filled = [&](uint32_t buf) {
+        wait(&acc_full[buf], (n >> 1) & 1u, dead);
+        dead = __any_sync(0xFFFFFFFFu, dead);
+        tc_fence_after();
+      };
+      constexpr int kChunks = SEG ? kCols / 16 : 1, kSides = SEG && GATED ? 2 : 1;
+      float sum[kSides][kChunks][16] = {};
+      if constexpr (SEG) {
+        int k0;
+        const int nk = steps_of(tl.split, k0);
+        for (int from = 0; from < nk && !dead; from += a.segment, ++n) {
+          const uint32_t buf = n & 1u;
+          filled(buf);
+          if (dead) break;
+#pragma unroll
+          for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+            for (int side = 0; side < kSides; ++side) {
+              uint32_t v[16];
+              tmem_ld16(column + buf * kTileN + side * (kTileN / 2) + 16 * i, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                sum[side][i][j] += __uint_as_float(v[j]);
+            }
+          drain(buf);
+        }
+      }
+      const uint32_t buf = n & 1u, at = column + buf * kTileN;
+      if constexpr (!SEG) filled(buf);
+      if (dead) break;
+      constexpr int kUnroll = SEG ? kChunks : 1;  // sums in registers need their places known
+#pragma unroll kUnroll
       for (int c = 0; c < kCols; c += 16) {
         uint32_t v[16], u[16];
         __syncwarp();
-        tmem_ld16(at + c, v);
-        if (GATED) tmem_ld16(at + kTileN / 2 + c, u);
-        tmem_ld_wait();
-        const int n0 = c_first + c;
-        if (a.splits > 1 || (a.vec && n0 + 16 <= l.N)) {
-          if (m < l.M) finish16<GATED>(a, tl.split, m, n0, v, u);
-          continue;
-        }
-        // rows of y that 16-byte pieces do not fit: two rows at a time, 16 columns each
-        float* turn = reinterpret_cast<float*>(smem + kStages * kStage + 512 + (w - 4) * kTurn);
-        float g[16];
+        if constexpr (SEG) {
 #pragma unroll
-        for (int p = 0; p < (GATED ? 2 : 1); ++p) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) turn[lane * 17 + j] = __uint_as_float(p ? u[j] : v[j]);
-          __syncwarp();
-          if (GATED && p == 0) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) g[i] = turn[(2 * i + (lane >> 4)) * 17 + (lane & 15)];
-            __syncwarp();
+          for (int j = 0; j < 16; ++j) {
+            v[j] = __float_as_uint(sum[0][(c / 16) % kChunks][j]);
+            if (GATED) u[j] = __float_as_uint(sum[kSides - 1][(c / 16) % kChunks][j]);
           }
+        } else {
+          tmem_ld16(at + c, v);
+          if (GATED) tmem_ld16(at + kTileN / 2 + c, u);
+          tmem_ld_wait();
         }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int r = 2 * i + (lane >> 4), n = n0 + (lane & 15);
-          const float f = turn[r * 17 + (lane & 15)];
-          const int row = m - lane + r;
-          if (row < l.M && n < l.N) linear_finish(l, a.row_scales, row, n, GATED ? g[i] : f, f);
-        }
-        __syncwarp();
+        float* turn = reinterpret_cast<float*>(smem + kStages * kStage + 512 + (w - 4) * kTurn);
+        if constexpr (SEG) output16_call<GATED>(a, tl.split, m, c_first + c, v, u, turn);
+        else output16<GATED>(a, tl.split, m, c_first + c, v, u, turn);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_cluster(leader_addr(&acc_empty[buf]));
+      if constexpr (!SEG) {
+        drain(buf);
+        ++n;
+      }
     }
   }
   __syncwarp();
@@ -475,12 +567,11 @@ __global__ void __launch_bounds__(256) linear_widen_kernel(const void* __restric
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-// fp32: at most this many 64-column steps of a product in one accumulator.  The tensor core
-// cuts its sums off, which pulls them towards zero by up to 2^-24 of the sum a step.
-constexpr int kF32Steps = 12;
+// fp32 outputs: 64-column steps that go through one accumulator at a time
+constexpr int kSegment = 12;
 
 struct TcLayout {
-  int mt, nt, ksteps, splits, pitch, np;
+  int mt, nt, ksteps, segment, splits, pitch, np;
   int xparts, wparts;
   bool w_copy;                // the weights are read from the workspace
   size_t x, w[2], partial, total;  // offsets in the workspace
@@ -488,7 +579,6 @@ struct TcLayout {
 TcLayout tc_layout(const moe_linear_desc& d, int M) {
   TcLayout t;
   const bool gated = d.W_up != nullptr, int4 = d.wfmt == MOE_W_INT4_B32 || d.wfmt == MOE_W_INT4_B128;
-  const bool f32 = d.xfmt == MOE_X_F32 || d.wfmt == MOE_W_F32;
   const int outs = gated ? kRows : 2 * kRows, sides = gated ? 2 : 1;
   t.xparts = d.xfmt == MOE_X_F32 ? 3 : 1;
   t.wparts = d.wfmt == MOE_W_F32 || (int4 && d.xfmt == MOE_X_F32) ? 3 : 1;
@@ -500,9 +590,11 @@ TcLayout tc_layout(const moe_linear_desc& d, int M) {
   // 74 pairs of SMs: split the reduction while the tiles leave half of them idle and a part
   // keeps 8 stages (the pipeline's fill) to work on
   const int steps = t.ksteps * (t.xparts == 1 ? t.wparts : (t.wparts == 1 ? t.xparts : 6));
+  const long long tiles = (long long)t.mt * t.nt;
   t.splits = 1;
-  while ((long long)t.mt * t.nt * t.splits * 2 <= 74 && steps >= 16 * t.splits && t.ksteps >= 2 * t.splits) t.splits *= 2;
-  if (f32) t.splits = std::max(t.splits, (t.ksteps + kF32Steps - 1) / kF32Steps);
+  if (tiles * 2 <= 74)
+    t.splits = std::max(1, std::min({(int)(74 / tiles), steps / 8, t.ksteps, 16}));
+  t.segment = d.yfmt == MOE_X_F32 ? kSegment : 0;
   t.w_copy = d.wfmt != MOE_W_BF16;
   const size_t wide = t.w_copy ? up256((size_t)t.wparts * d.N * t.pitch * 2) : 0;
   t.w[0] = 0;
@@ -517,7 +609,7 @@ TcLayout tc_layout(const moe_linear_desc& d, int M) {
 
 bool linear_tc_ok(const moe_linear_desc& d, int M) {
   const bool f32 = d.xfmt == MOE_X_F32 || d.wfmt == MOE_W_F32;
-  return M > (f32 ? kLinearRowTokens : kLinearStreamTokens);
+  return M > (f32 ? kLinearRowTokens : linear_stream_tokens(d.wfmt));
 }
 
 size_t linear_tc_workspace(const moe_linear_desc& d, int M) { return tc_layout(d, M).total; }
@@ -559,7 +651,7 @@ static TcArgs tc_args(const moe_linear_desc& d, const LinearArgs& a, const TcLay
   TcArgs p = {};
   p.l = a;
   p.row_scales = d.wfmt == MOE_W_INT8_ROW;
-  p.mt = t.mt, p.nt = t.nt, p.splits = t.splits, p.ksteps = t.ksteps;
+  p.mt = t.mt, p.nt = t.nt, p.splits = t.splits, p.ksteps = t.ksteps, p.segment = t.segment;
   p.xparts = t.xparts, p.wparts = t.wparts, p.np = t.np;
   const int yb = d.yfmt == MOE_X_F32 ? 4 : 2;
   auto pieces = [&](const void* q, long long ld) { return reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld * yb % 16 == 0; };
@@ -583,9 +675,12 @@ cudaError_t launch_linear_tc(const moe_linear_desc& d, const LinearArgs& a, void
                   (uint64_t)d.N * t.wparts, t.wparts == 3 ? (uint64_t)t.pitch * 2 : (uint64_t)d.K * 2, kK, kRows,
                   CU_TENSOR_MAP_SWIZZLE_128B);
   if (!gated) mw[1] = mw[0];
-  auto kernel = gated ? linear_tc_kernel<true> : linear_tc_kernel<false>;
-  static std::atomic<bool> allowed[2][64];
-  if (e == cudaSuccess) e = allow_smem(reinterpret_cast<const void*>(kernel), kSmem, allowed[gated]);
+  // a split that is one segment long needs no segments
+  const bool seg = t.segment > 0 && (t.ksteps + t.splits - 1) / t.splits > t.segment;
+  auto kernel = gated ? (seg ? linear_tc_kernel<true, true> : linear_tc_kernel<true, false>)
+                      : (seg ? linear_tc_kernel<false, true> : linear_tc_kernel<false, false>);
+  static std::atomic<bool> allowed[4][64];
+  if (e == cudaSuccess) e = allow_smem(reinterpret_cast<const void*>(kernel), kSmem, allowed[2 * seg + gated]);
   if (e != cudaSuccess) return e;
   const long long tiles = (long long)t.mt * t.nt * t.splits;
   const int pairs = (int)std::min<long long>(tiles, num_sms / 2);

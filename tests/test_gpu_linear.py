@@ -40,8 +40,9 @@ class Product:
         return torch.from_numpy(synth.normal_f32((M, self.N), seed, 9, 0.0, 1.0)).to(self.y_dtype)
 
     def judge(self, x, y, residual=None, what=""):
-        # the library widens int4 weights exactly below this many rows (see moe_linear)
-        exact = x.shape[0] <= 64
+        # int4 weights are widened exactly for up to 16 tokens; beyond, each is rounded to bf16 once,
+        # which is off by half a step of bf16 at most (moe_linear)
+        exact = x.shape[0] <= 16
         want, bound = ref.linear(x, self.W, self.b, None if self.Wu is None else (self.Wu, self.bu), self.act, residual,
                                  self.y_dtype, self.wfmt, exact)
         ref.check(y, want, bound, what)
@@ -56,7 +57,7 @@ class Product:
 
 
 @pytest.mark.parametrize("wfmt,xfmt", FORMATS)
-@pytest.mark.parametrize("M", [1, 7, 16, 40, 64, 65, 200])
+@pytest.mark.parametrize("M", [1, 7, 16, 17, 32, 33, 40, 64, 65, 200])
 def test_formats(wfmt, xfmt, M):
     Product(384, 200, wfmt, xfmt, bias=True, act="silu").run(M, residual=M % 2 == 0)
 
