@@ -54,7 +54,8 @@ template <int XF, int TT>
 __global__ void __launch_bounds__(kRouterThreads)
     few_router_kernel(const void* __restrict__ x, const float* __restrict__ W_r, const float* __restrict__ bias,
                       const uint8_t* __restrict__ mask, int T, int H, int E, int router, uint64_t* __restrict__ keys,
-                      double* __restrict__ scores, uint32_t* __restrict__ counters, uint32_t* flags) {
+                      double* __restrict__ scores, uint32_t* __restrict__ counters, int8_t* __restrict__ digits, int int4,
+                      float* __restrict__ units, uint32_t* flags) {
   pdl_wait();
   pdl_trigger();
   constexpr int kSums = kRouterExperts * TT, kRWarps = kRouterThreads / 32;
@@ -62,6 +63,15 @@ __global__ void __launch_bounds__(kRouterThreads)
   const int e0 = blockIdx.x * kRouterExperts, tid = threadIdx.x, w = warp_id(), lane = lane_id();
   if (blockIdx.x == 0)
     for (int i = tid; i < kFewCounters; i += kRouterThreads) counters[i] = 0;
+  if (e0 >= E) {
+    // the CTAs past the experts: a token each, as digits for the integer products
+    const int t = blockIdx.x - (E + kRouterExperts - 1) / kRouterExperts;
+    __shared__ float warps[kRouterThreads / 32];
+    if constexpr (XF == MOE_X_BF16)
+      stream::write_digits(static_cast<const uint16_t*>(x) + (size_t)t * H, H, int4, digits + (size_t)t * 4 * stream::digit_pitch(H),
+                           units + t, warps);
+    return;
+  }
   const float* row[kRouterExperts];
 #pragma unroll
   for (int i = 0; i < kRouterExperts; ++i) row[i] = W_r + (size_t)min(e0 + i, E - 1) * H;
@@ -137,6 +147,8 @@ struct FewArgs {
   const float* s[3];
   const void* Ws[3];  // and of the shared expert
   const float* ss[3];
+  const int8_t* digits;  // [T][4][digit_pitch(H)] and the tokens' units: quantised weights on the streaming path
+  const float* units;
   const uint64_t* keys;
   const double* scores;
   float* h;           // [T k, I] of the routed pairs, then [T, Is] of the shared expert
@@ -400,13 +412,15 @@ __global__ void __launch_bounds__(kFewThreads) few_layer_kernel(const FewArgs a)
 constexpr int kWarps = 12;
 constexpr int kStreamThreads = 32 * kWarps;
 constexpr int kMaxPairs = MOE_FEW_MAX_TOKENS * 32;
-constexpr int kUpTokens = 8;    // tokens of a gate/up unit
 constexpr int kDownTokens = 4;  // tokens of a down tile: values in columns 0..3, remainders in 4..7
 constexpr int kMaxStages = 4;
 
 template <int WF>
 struct Ring {
   using F = stream::Format<WF>;
+  static constexpr bool kDigits = WF != MOE_W_BF16;       // gate/up products are integer ones
+  static constexpr int kUpTiles = kDigits ? 2 : 1;        // token tiles of a gate/up unit
+  static constexpr int kUpTokens = kDigits ? kUpTiles * stream::kDigitTokens : 8;
   static constexpr int kStage = 2 * (stream::kBoxBytes + F::kScaleBox);  // gate and up box, or down boxes
   static constexpr int kDownBoxes = F::kInt4 ? 1 : 2;                    // of a stage (bounds the tokens loaded ahead)
   static constexpr int kStages = F::kScaleBoxes ? 3 : kMaxStages;
@@ -437,9 +451,9 @@ struct StreamShared {
   uint16_t lists[kFewLists];     // this CTA's lists
   float pair_w[kMaxPairs];
   uint16_t pair[kMaxPairs];      // valid pairs in expert order: pair | token << 9
-  uint32_t up[kMaxPairs + 2], down[kMaxPairs + 4];  // entries: shared first / shared last
-  union {
-    float4 part[2][kWarps][2][32];             // [unit parity][warp][gate, up]
+  uint32_t up[kMaxPairs + 4], down[kMaxPairs + 4];  // entries: shared first / shared last
+  union alignas(16) {            // read in pieces of 16 bytes
+    float part[2][kWarps][2][16][8];           // [unit parity][warp][gate, up][row][token]
     float y[kWarps][MOE_FEW_MAX_TOKENS][16];   // down: each warp's share of 16 rows
     struct {
       int e[kMaxPairs];                        // building the plan: by pair
@@ -448,6 +462,8 @@ struct StreamShared {
     } plan;
   };
 };
+
+static_assert(offsetof(StreamShared, plan) % 16 == 0 && offsetof(StreamShared, part) % 16 == 0, "alignment");
 
 __device__ __forceinline__ void few_wait(uint64_t* bar, uint32_t parity, bool& dead, uint32_t* flags) {
   if (dead) return;
@@ -477,6 +493,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     few_stream_kernel(const __grid_constant__ FewMaps maps, const __grid_constant__ FewArgs a) {
   using R = Ring<WF>;
   using F = stream::Format<WF>;
+  constexpr int kUpTokens = R::kUpTokens;
   extern __shared__ uint8_t smem[];
   // the rings first, on 1,024 bytes (the swizzle's period)
   uint8_t* rings = smem + (((smem_u32(smem) + 1023u) & ~1023u) - smem_u32(smem));
@@ -698,7 +715,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   // ---------------------------------------------------------------- gate and up
   int n_lists = 0, events = 0;
   for (int list = sh.taken ? -1 : (int)blockIdx.x; list >= 0;) {
-    float acc[2][4] = {};
+    using Sum = std::conditional_t<R::kDigits, stream::DigitSum<WF>, float>;
+    Sum acc[2][R::kUpTiles][4] = {};
     UpWalk unit = first_unit(list, 0);  // the next to hand over
     // this warp's sums of the unit to shared memory; the warp whose turn it is adds them up
     auto hand_over = [&] {
@@ -708,11 +726,21 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       few_wait(&sh.rempty[up_team][buf], parity ^ 1, dead, a.flags);
       if (shares == a.team || (up_w >= from ? up_w - from : up_w + a.team - from) < shares) {
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          sh.part[buf][w][mt][lane] = make_float4(acc[mt][0], acc[mt][1], acc[mt][2], acc[mt][3]);
+        for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) acc[mt][k] = 0.f;
-        }
+          for (int nt = 0; nt < R::kUpTiles; ++nt) {
+            float(&p)[16][8] = sh.part[buf][w][mt];
+            if constexpr (R::kDigits) {
+              float r0, r8;
+              stream::join_digits(acc[mt][nt], r0, r8);
+              if ((c & 1) == 0) p[g][2 * nt + c / 2] = r0, p[g + 8][2 * nt + c / 2] = r8;
+            } else {
+              *reinterpret_cast<float2*>(&p[g][2 * c]) = make_float2(acc[mt][nt][0], acc[mt][nt][1]);
+              *reinterpret_cast<float2*>(&p[g + 8][2 * c]) = make_float2(acc[mt][nt][2], acc[mt][nt][3]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[mt][nt][k] = 0;
+          }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.rfull[up_team][buf]);
@@ -729,10 +757,13 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 #pragma unroll
             for (int r = 0; r < 2; ++r) scale[mt][r] = __ldg((shared ? a.ss[mt] : a.s[mt]) + row + 8 * r);
         }
+        float unit_x[2] = {1.f, 1.f};
         size_t to[2];  // where the two tokens' h go
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int j = min(2 * c + i, m - 1);
+          if constexpr (R::kDigits)
+            unit_x[i] = a.units[shared ? start + j : sh.pair[start + j] >> 9] * (F::kInt4 ? 0.0625f : 1.f);
           to[i] = (shared ? (size_t)P * a.I + (size_t)(start + j) * a.Is : (size_t)(sh.pair[start + j] & 511) * a.I) + i0;
         }
         few_wait(&sh.rfull[up_team][buf], parity, dead, a.flags);
@@ -742,8 +773,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         for (int i = 0; i < shares; ++i, s = s + 1 == a.team ? 0 : s + 1) {
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt) {
-            const float4 p = sh.part[buf][up_team * a.team + s][mt][lane];
-            sum[mt][0] += p.x, sum[mt][1] += p.y, sum[mt][2] += p.z, sum[mt][3] += p.w;
+            const float(&p)[16][8] = sh.part[buf][up_team * a.team + s][mt];
+            const float2 r0 = *reinterpret_cast<const float2*>(&p[g][2 * c]), r8 = *reinterpret_cast<const float2*>(&p[g + 8][2 * c]);
+            sum[mt][0] += r0.x, sum[mt][1] += r0.y, sum[mt][2] += r8.x, sum[mt][3] += r8.y;
           }
         }
         __syncwarp();
@@ -751,7 +783,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           if (2 * c + (k & 1) >= m) continue;
-          const float gate = sum[0][k] * scale[0][k >> 1], up = sum[1][k] * scale[1][k >> 1];
+          const float gate = sum[0][k] * (scale[0][k >> 1] * unit_x[k & 1]), up = sum[1][k] * (scale[1][k >> 1] * unit_x[k & 1]);
           const float h = a.act == MOE_ACT_SILU ? silu_mul(gate, up) : gelu_tanh_mul(gate, up);
           const uint16_t hi = f32_to_bf16(h);
           const float rest = h - bf16_to_f32(hi);
@@ -765,17 +797,39 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     };
     UpWalk at = first_unit(list, up_w);
     seek_up(at);
-    uint4 x[F::kLoads], x_next[F::kLoads];
-    const uint16_t* tok = nullptr;  // the lane's token, of the unit at `at`
-    size_t row = 0;                 // int4: row of the block scales
+    // the lane's token columns: bf16, or a digit of each tile's token
+    using Columns = std::conditional_t<R::kDigits, stream::Digits<WF>, stream::Bf16Columns<WF>>;
+    Columns x[R::kUpTiles], x_next[R::kUpTiles];
+    const char* tok[R::kUpTiles] = {};  // of the unit at `at`
+    int tiles = 1, tiles_next = 1;
+    size_t row = 0;                     // int4: row of the block scales
     auto unit_of = [&] {
       const uint32_t en = sh.up[at.entry];
-      const int j = entry_start(en) + min(g, entry_n(en) - 1);  // columns past the tokens are not used
-      const int t = at.entry < su ? j : sh.pair[j] >> 9;
-      tok = static_cast<const uint16_t*>(a.x) + (size_t)t * a.H;
+      const int m = entry_n(en);
+      tiles_next = R::kDigits ? (m + stream::kDigitTokens - 1) / stream::kDigitTokens : 1;
+#pragma unroll
+      for (int nt = 0; nt < R::kUpTiles; ++nt) {
+        // columns past the tokens are not used
+        const int j = entry_start(en) + min(R::kDigits ? stream::kDigitTokens * nt + g / 4 : g, m - 1);
+        const int t = at.entry < su ? j : sh.pair[j] >> 9;
+        if constexpr (R::kDigits)
+          tok[nt] = reinterpret_cast<const char*>(a.digits) + ((size_t)t * 4 + (g & 3)) * stream::digit_pitch(a.H);
+        else
+          tok[nt] = reinterpret_cast<const char*>(static_cast<const uint16_t*>(a.x) + (size_t)t * a.H);
+      }
       if constexpr (F::kInt4) row = (at.entry < su ? 0 : (size_t)entry_e(en) * a.I) + at.block * 16 + g;
     };
-    auto fetch = [&] { stream::load_token<WF>(tok + at.j * F::kBoxCols, a.H - at.j * F::kBoxCols, x_next); };
+    auto fetch = [&] {
+#pragma unroll
+      for (int nt = 0; nt < R::kUpTiles; ++nt) {
+        if (nt >= tiles_next) break;
+        if constexpr (R::kDigits)
+          stream::load_digits<WF>(reinterpret_cast<const int8_t*>(tok[nt]) + at.j * F::kBoxCols, x_next[nt]);
+        else
+          stream::load_token<WF>(reinterpret_cast<const uint16_t*>(tok[nt]) + at.j * F::kBoxCols, a.H - at.j * F::kBoxCols,
+                                 x_next[nt].v);
+      }
+    };
     if (at.entry < n_up) {
       unit_of();
       fetch();
@@ -786,7 +840,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       while (more ? unit.n < at.n : unit.entry < n_up) hand_over();
       if (!more) break;
 #pragma unroll
-      for (int i = 0; i < F::kLoads; ++i) x[i] = x_next[i];
+      for (int nt = 0; nt < R::kUpTiles; ++nt) x[nt] = x_next[nt];
+      tiles = tiles_next;
       const uint32_t stage = smem_u32(ring + out_slot * R::kStage);
       stream::Scales sc[2];
       if constexpr (F::kInt4) {
@@ -808,7 +863,12 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       }
       if (at.entry < n_up) fetch();
       landed();
-      stream::mac_box<WF, 2>(stage, x, sc, acc);
+      if constexpr (R::kDigits) {
+        stream::mac_box_digits<WF, 2, R::kUpTiles>(stage, tiles, x, sc, acc);
+      } else {
+        float(&sums)[2][4] = reinterpret_cast<float(&)[2][4]>(acc);
+        stream::mac_box<WF, 2>(stage, x[0].v, sc, sums);
+      }
       read();
     }
     if (threadIdx.x == 0) sh.lists[n_lists] = (uint16_t)list;
@@ -996,15 +1056,20 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   }
 }
 
+// bf16 tokens on quantised weights: the gate/up products are integer ones
+bool few_digits(const moe_desc& d) { return d.xfmt == MOE_X_BF16 && d.wfmt >= MOE_W_INT8_ROW; }
+
 struct FewLayout {
-  size_t keys, scores, h, total;
+  size_t keys, scores, digits, units, h, total;
 };
 FewLayout few_layout(const moe_desc& d, int Is, int T) {
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   FewLayout l;
   l.keys = up(kFewCounters * sizeof(uint32_t));
   l.scores = l.keys + up((size_t)T * d.E * 8);
-  l.h = l.scores + up((size_t)T * d.E * 8);
+  l.digits = l.scores + up((size_t)T * d.E * 8);
+  l.units = l.digits + (few_digits(d) ? up((size_t)T * 4 * stream::digit_pitch(d.H)) : 0);
+  l.h = l.units + up((size_t)T * 4);
   l.total = l.h + up(((size_t)T * d.k * d.I + (size_t)T * Is) * 4);
   return l;
 }
@@ -1075,9 +1140,11 @@ cudaError_t launch_few_router(const moe_desc& d, const moe_shared_expert* sh, co
   const FewLayout l = few_layout(d, sh ? sh->I : 0, T);
   char* ws = static_cast<char*>(workspace);
   auto go = [&](auto kernel) {
-    return launch_k(kernel, dim3((d.E + kRouterExperts - 1) / kRouterExperts), dim3(kRouterThreads), 0, s, x, d.W_r, d.b,
-                    d.expert_mask, T, d.H, d.E, d.router, reinterpret_cast<uint64_t*>(ws + l.keys),
-                    reinterpret_cast<double*>(ws + l.scores), reinterpret_cast<uint32_t*>(ws), flags);
+    const int ctas = (d.E + kRouterExperts - 1) / kRouterExperts + (few_digits(d) ? T : 0);
+    return launch_k(kernel, dim3(ctas), dim3(kRouterThreads), 0, s, x, d.W_r, d.b, d.expert_mask, T, d.H, d.E, d.router,
+                    reinterpret_cast<uint64_t*>(ws + l.keys), reinterpret_cast<double*>(ws + l.scores),
+                    reinterpret_cast<uint32_t*>(ws), reinterpret_cast<int8_t*>(ws + l.digits),
+                    (int)(d.wfmt != MOE_W_INT8_ROW), reinterpret_cast<float*>(ws + l.units), flags);
   };
   if (d.xfmt == MOE_X_F32)
     return T == 1 ? go(few_router_kernel<MOE_X_F32, 1>) : (T <= 4 ? go(few_router_kernel<MOE_X_F32, 4>) : go(few_router_kernel<MOE_X_F32, 8>));
@@ -1110,6 +1177,8 @@ cudaError_t launch_few_layer(const moe_desc& d, const moe_shared_expert* sh, con
     a.boxed[2] = boxed_scales(d.wfmt, sh->s_gate, d.H) && boxed_scales(d.wfmt, sh->s_up, d.H);
     a.boxed[3] = boxed_scales(d.wfmt, sh->s_down, sh->I);
   }
+  a.digits = reinterpret_cast<const int8_t*>(ws + l.digits);
+  a.units = reinterpret_cast<const float*>(ws + l.units);
   a.counters = reinterpret_cast<uint32_t*>(ws);
   a.idx = idx, a.w = w, a.y = y, a.flags = flags;
   switch (d.wfmt) {

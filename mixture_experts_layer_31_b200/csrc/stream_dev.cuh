@@ -14,7 +14,17 @@
 //   int4  the code (q + 8) goes into the upper mantissa bits of 16: 16 + (q + 8) = q + 24;
 //         an instruction with -24 in every place of the weights takes 24 x out again
 // int8 rows are scaled in the caller's epilogue, int4 blocks here, in fp32.
+//
+// Widening takes more instructions than everything else.  Where a token can be prepared
+// beforehand (mac_box_digits) the codes stay integers and the token becomes four signed
+// digits of 8 bits,  x = 2^(e - 30) (d0 + 2^8 d1 + 2^16 d2 + 2^24 d3),  |x| < 2^e for the whole
+// token, each digit a column of its own of an integer matrix instruction: sums are exact,
+// and only the rounding of x to 2^(e - 31) (the 31st bit below the token's largest value; a
+// bf16 value keeps all its bits down to 2^-22 of that) stands for the 8 bits of each bf16
+// product.  Measured on 16 tokens: 256 us with widened codes, see the layer's kernel.
 #pragma once
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace moe {
@@ -302,6 +312,173 @@ __device__ __forceinline__ void mac_box_tiles(uint32_t boxes, int ntiles, Load l
       }
     }
   }
+}
+
+// ---------------------------------------------------------------- tokens as digits
+
+// d = a b + c, signed 8-bit integers, 32 columns of the reduction
+__device__ __forceinline__ void imma16832(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1, int c0, int c1, int c2, int c3) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(c0), "r"(c1), "r"(c2), "r"(c3));
+}
+
+constexpr int kDigitTokens = 2;  // of a tile: column 4 t + d is digit d of token t
+// bytes of a digit's row: whole boxes, so that no load has to ask where the columns end (the
+// weights past them read as zero)
+__host__ __device__ inline int digit_pitch(int K) { return (K + 255) / 256 * 256; }
+
+// A token's digits, [4][pitch], and what a unit of the lowest one stands for, by one block.
+// int4: the even columns of each 8 come before the odd ones, as the codes are taken apart.
+// A token with an infinity or NaN becomes NaN as a whole.
+__device__ __forceinline__ void write_digits(const uint16_t* x, int K, bool int4, int8_t* out, float* unit, float* smem) {
+  const int tid = threadIdx.x, threads = blockDim.x, pitch = digit_pitch(K);
+  float m = 0.f;
+  bool bad = false;
+  for (int c = tid * 8; c < K; c += threads * 8) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(x + c));
+    const uint32_t word[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float a = fabsf(bf16_to_f32(word[j] & 0xFFFFu)), b = fabsf(__uint_as_float(word[j] & 0xFFFF0000u));
+      m = fmaxf(m, fmaxf(a, b));
+      bad |= !isfinite(a) || !isfinite(b);
+    }
+  }
+  // magnitudes are ordered like their bits; a value that is not finite is above all
+  uint32_t bits = bad ? 0x7F800000u : __float_as_uint(m);
+  bits = __reduce_max_sync(0xFFFFFFFFu, bits);
+  if (lane_id() == 0) smem[warp_id()] = __uint_as_float(bits);
+  __syncthreads();
+  for (int w = 0; w < threads / 32; ++w) bits = max(bits, __float_as_uint(smem[w]));
+  const bool finite = bits < 0x7F800000u;
+  const int e = max((int)(bits >> 23) - 126, -90);  // |x| < 2^e; what lies below 2^-121 is dropped
+  const float scale = __uint_as_float((uint32_t)(127 + 30 - e) << 23);
+  if (tid == 0) *unit = finite ? __uint_as_float((uint32_t)(127 - 30 + e) << 23) : __uint_as_float(0x7FC00000u);
+  for (int c = tid * 8; c < pitch; c += threads * 8) {
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (c < K && finite) u = __ldg(reinterpret_cast<const uint4*>(x + c));
+    const uint32_t word[4] = {u.x, u.y, u.z, u.w};
+    uint32_t d[4][2] = {};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float f = (j & 1) ? __uint_as_float(word[j >> 1] & 0xFFFF0000u) : bf16_to_f32(word[j >> 1] & 0xFFFFu);
+      int v = __float2int_rn(f * scale);
+      const int at = int4 ? (j >> 1) + 4 * (j & 1) : j;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int digit = (int)(int8_t)v;
+        d[k][at >> 2] |= (uint32_t)(digit & 255) << (8 * (at & 3));
+        v = (v - digit) >> 8;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) *reinterpret_cast<uint2*>(out + (size_t)k * pitch + c) = make_uint2(d[k][0], d[k][1]);
+  }
+  __syncthreads();
+}
+
+template <int WF>
+struct Bf16Columns {
+  uint4 v[Format<WF>::kLoads];
+};
+
+// The lane's digits for one box: 2 x 16 bytes (int8: units 2c and 2c + 1) or 8 x 8 bytes (int4: word
+// c of each unit); `row` is the digit's row of the lane's token, from the box's first column on.
+template <int WF>
+struct Digits {
+  uint32_t v[Format<WF>::kInt4 ? 16 : 8];
+};
+template <int WF>
+__device__ __forceinline__ void load_digits(const int8_t* row, Digits<WF>& x) {
+  const int c = lane_id() & 3;
+  if constexpr (Format<WF>::kInt4) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const uint2 p = *reinterpret_cast<const uint2*>(row + 32 * u + 8 * c);
+      x.v[2 * u] = p.x, x.v[2 * u + 1] = p.y;
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint4 p = *reinterpret_cast<const uint4*>(row + 32 * c + 16 * h);
+      x.v[4 * h] = p.x, x.v[4 * h + 1] = p.y, x.v[4 * h + 2] = p.z, x.v[4 * h + 3] = p.w;
+    }
+  }
+}
+
+// Sums by digit: int8 the whole reduction as integers (at most 2^14 a column, 65,536 columns),
+// int4 in fp32 with the block scales applied, 16 times too large.
+template <int WF>
+using DigitSum = std::conditional_t<Format<WF>::kInt4, float, int>;
+
+// acc[mt][nt] += box mt times the digits of tile nt < ntiles
+template <int WF, int MT, int NT>
+__device__ __forceinline__ void mac_box_digits(uint32_t boxes, int ntiles, const Digits<WF> (&x)[NT], const Scales (&sc)[MT],
+                                               DigitSum<WF> (&acc)[MT][NT][4]) {
+  using F = Format<WF>;
+  const int g = lane_id() >> 2, c = lane_id() & 3;
+  const uint32_t row = boxes + g * 128;
+  if constexpr (!F::kInt4) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t at = row + (((2 * c + h) ^ g) << 4);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const uint4 a = ld_shared_v4(at + mt * kBoxBytes), b = ld_shared_v4(at + mt * kBoxBytes + 1024);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if (nt >= ntiles) break;
+          int(&d)[4] = acc[mt][nt];
+          imma16832(d, a.x, b.x, a.y, b.y, x[nt].v[4 * h], x[nt].v[4 * h + 1], d[0], d[1], d[2], d[3]);
+          imma16832(d, a.z, b.z, a.w, b.w, x[nt].v[4 * h + 2], x[nt].v[4 * h + 3], d[0], d[1], d[2], d[3]);
+        }
+      }
+    }
+  } else {
+    // 2^23 + 2^22 as bits: added to an integer below 2^22 it makes the float 12582912 + the integer
+    constexpr int kOne = 0x4B400000;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float s0[MT][4], s8[MT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) load_block_scales<WF>(sc[mt], h, s0[mt], s8[mt]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t at = row + (((4 * h + i) ^ g) << 4) + 4 * c;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const uint32_t a = ld_shared_u32(at + mt * kBoxBytes), b = ld_shared_u32(at + mt * kBoxBytes + 1024);
+          // a code in the upper half of a byte is 16 times itself: low nibbles (even columns), high ones
+          const uint32_t al = (a << 4) & 0xF0F0F0F0u, ah = a & 0xF0F0F0F0u;
+          const uint32_t bl = (b << 4) & 0xF0F0F0F0u, bh = b & 0xF0F0F0F0u;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            if (nt >= ntiles) break;
+            int d[4];
+            imma16832(d, al, bl, ah, bh, x[nt].v[8 * h + 2 * i], x[nt].v[8 * h + 2 * i + 1], kOne, kOne, kOne, kOne);
+            acc[mt][nt][0] = fmaf(__int_as_float(d[0]) - 12582912.f, s0[mt][i], acc[mt][nt][0]);
+            acc[mt][nt][1] = fmaf(__int_as_float(d[1]) - 12582912.f, s0[mt][i], acc[mt][nt][1]);
+            acc[mt][nt][2] = fmaf(__int_as_float(d[2]) - 12582912.f, s8[mt][i], acc[mt][nt][2]);
+            acc[mt][nt][3] = fmaf(__int_as_float(d[3]) - 12582912.f, s8[mt][i], acc[mt][nt][3]);
+          }
+        }
+      }
+    }
+  }
+}
+
+// The four digits of a token put together: rows g (r0) and g + 8 (r8) of token lane % 4 / 2, in both
+// lanes of a pair.  To be multiplied by the token's unit (and int4 by 1/16).
+template <typename T>
+__device__ __forceinline__ void join_digits(const T (&acc)[4], float& r0, float& r8) {
+  const bool high = lane_id() & 1;  // the lane's columns are digits 0 and 1, or 2 and 3
+  const float w0 = high ? 65536.f : 1.f, w1 = high ? 16777216.f : 256.f;
+  r0 = fmaf((float)acc[1], w1, (float)acc[0] * w0);
+  r8 = fmaf((float)acc[3], w1, (float)acc[2] * w0);
+  r0 += __shfl_xor_sync(0xFFFFFFFFu, r0, 1);
+  r8 += __shfl_xor_sync(0xFFFFFFFFu, r8, 1);
 }
 
 }  // namespace stream
