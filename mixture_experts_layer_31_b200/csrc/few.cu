@@ -515,13 +515,6 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     if (a.Is) prefetch_tmap(&maps.ws[w]);
   }
   __syncthreads();
-  pdl_wait();
-  pdl_trigger();
-  if (threadIdx.x == 0) {
-    atomicAdd(&a.counters[0], 1u);
-    sh.taken = atomicExch(&a.counters[kFewOwner + blockIdx.x], 1u) != 0;
-  }
-
   const int P = a.T * a.k, grid = (int)gridDim.x;
   const int su = a.Is ? (a.T + kUpTokens - 1) / kUpTokens : 0, sd = a.Is ? (a.T + kDownTokens - 1) / kDownTokens : 0;
   const int sb = a.Is / 16, ub = a.I / 16, hb = a.H / 16;  // blocks of 16 rows
@@ -633,8 +626,16 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       seek_down(head_down);
     }
   };
-  // the shared expert's units need no routing: their copies run while the plan is made
+  // The shared expert's units need no routing, and weights are nothing that the launch before this
+  // one writes: their copies start before its end is waited for.  (Launches before that one
+  // are over: it lets this one start only after its own wait.)
   while (issued < R::kStages && head.entry < n_up) issue_up();
+  pdl_wait();
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    atomicAdd(&a.counters[0], 1u);
+    sh.taken = atomicExch(&a.counters[kFewOwner + blockIdx.x], 1u) != 0;
+  }
 
   // the plan: routing, the pairs in expert order, entries of up to 8 (gate/up) and 4 (down) tokens
   for (int t = w; t < a.T; t += kWarps) {
@@ -839,9 +840,11 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       const bool more = at.entry < n_up;
       while (more ? unit.n < at.n : unit.entry < n_up) hand_over();
       if (!more) break;
-#pragma unroll
-      for (int nt = 0; nt < R::kUpTiles; ++nt) x[nt] = x_next[nt];
       tiles = tiles_next;
+      x[0] = x_next[0];
+#pragma unroll
+      for (int nt = 1; nt < R::kUpTiles; ++nt)
+        if (nt < tiles) x[nt] = x_next[nt];
       const uint32_t stage = smem_u32(ring + out_slot * R::kStage);
       stream::Scales sc[2];
       if constexpr (F::kInt4) {
@@ -852,8 +855,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           sc[mt].box = stage + 2 * stream::kBoxBytes + mt * F::kScaleBox;
           sc[mt].in_box = a.boxed[shared ? 2 : 0];
           sc[mt].left = a.H - at.j * F::kBoxCols;
-          sc[mt].s0 = (shared ? a.ss[mt] : a.s[mt]) + row * pitch + (at.j * F::kBoxCols >> F::kScaleShift);
-          sc[mt].s8 = sc[mt].s0 + 8 * pitch;
+          if (!sc[mt].in_box) {
+            sc[mt].s0 = (shared ? a.ss[mt] : a.s[mt]) + row * pitch + (at.j * F::kBoxCols >> F::kScaleShift);
+            sc[mt].s8 = sc[mt].s0 + 8 * pitch;
+          }
         }
       }
       at.j += a.team;
@@ -989,8 +994,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           sc[d][0].box = stage + 2 * stream::kBoxBytes + d * F::kScaleBox;
           sc[d][0].in_box = a.boxed[entry_e(en) == kSharedEntry ? 3 : 1];
           sc[d][0].left = left - d * F::kBoxCols;
-          sc[d][0].s0 = s0 + (c0 + d * F::kBoxCols >> F::kScaleShift);
-          sc[d][0].s8 = sc[d][0].s0 + 8 * (size_t)(K >> F::kScaleShift);
+          if (!sc[d][0].in_box) {
+            sc[d][0].s0 = s0 + (c0 + d * F::kBoxCols >> F::kScaleShift);
+            sc[d][0].s8 = sc[d][0].s0 + 8 * (size_t)(K >> F::kScaleShift);
+          }
         }
       }
       // the next stage's tokens, of the same entry or of the next

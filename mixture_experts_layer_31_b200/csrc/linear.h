@@ -53,7 +53,12 @@ __device__ __forceinline__ void linear_finish(const LinearArgs& a, bool row_scal
 }
 
 bool linear_stream_ok(const moe_linear_desc& d, int M);
-cudaError_t launch_linear_stream(const moe_linear_desc& d, const LinearArgs& a, int num_sms, uint32_t* flags, cudaStream_t s);
+bool linear_stream_digits(const moe_linear_desc& d, int M);        // the tokens are taken as digits
+bool linear_stream_digits_first(const moe_linear_desc& d, int M);  // which a launch before it makes
+size_t linear_stream_workspace(const moe_linear_desc& d, int M);
+cudaError_t launch_linear_digits(const moe_linear_desc& d, const LinearArgs& a, void* workspace, cudaStream_t s);
+cudaError_t launch_linear_stream(const moe_linear_desc& d, const LinearArgs& a, void* workspace, int num_sms, uint32_t* flags,
+                                 cudaStream_t s);
 // fp32 tokens or weights: up to this many tokens a warp computes rows of W in fp32
 constexpr int kLinearRowTokens = 16;
 cudaError_t launch_linear_rows(const moe_linear_desc& d, const LinearArgs& a, int num_sms, cudaStream_t s);

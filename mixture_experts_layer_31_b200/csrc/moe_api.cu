@@ -670,7 +670,8 @@ static moe_status validate_linear(const moe_linear_desc* d, int32_t M) {
 }
 
 size_t moe::linear_workspace_bytes(const moe_linear_desc& d, int M) {
-  return linear_tc_ok(d, M) ? linear_tc_workspace(d, M) : 0;
+  if (M <= 0) return 0;
+  return linear_tc_ok(d, M) ? linear_tc_workspace(d, M) : linear_stream_workspace(d, M);
 }
 
 extern "C" moe_status moe_linear_workspace_size(const moe_linear_desc* d, int32_t M, size_t* bytes) {
@@ -708,7 +709,9 @@ extern "C" moe_status moe_linear(const moe_linear_desc* d, const void* x, int64_
   a.x = x, a.ldx = ldx, a.residual = residual, a.ldr = ldr, a.y = y, a.ldy = ldy;
   a.W[0] = d->W, a.W[1] = d->W_up, a.s[0] = d->s, a.s[1] = d->s_up, a.b[0] = d->b, a.b[1] = d->b_up;
   if (linear_stream_ok(*d, M)) {
-    MOE_LAUNCH("linear_stream", stream, launch_linear_stream(*d, a, dev->num_sms, dev->flags, stream));
+    if (linear_stream_digits_first(*d, M))
+      MOE_LAUNCH("linear_digits", stream, launch_linear_digits(*d, a, workspace, stream));
+    MOE_LAUNCH("linear_stream", stream, launch_linear_stream(*d, a, workspace, dev->num_sms, dev->flags, stream));
     return MOE_OK;
   }
   if (linear_tc_ok(*d, M)) {
