@@ -614,6 +614,15 @@ bool linear_tc_ok(const moe_linear_desc& d, int M) {
 
 size_t linear_tc_workspace(const moe_linear_desc& d, int M) { return tc_layout(d, M).total; }
 
+// The launches of one call follow one another closely: each may start while the one before it
+// finishes, and waits for its end before it touches memory.
+template <typename... KArgs, typename... Args>
+static cudaError_t launch_next(bool first, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                               Args&&... args) {
+  return first ? launch_k(kernel, grid, block, smem, s, static_cast<Args&&>(args)...)
+               : launch_k_after(kernel, grid, block, smem, s, static_cast<Args&&>(args)...);
+}
+
 static dim3 grid_for(size_t items, int num_sms) {
   return dim3((unsigned)std::min<size_t>((items + 255) / 256, (size_t)num_sms * 8));
 }
@@ -626,7 +635,9 @@ cudaError_t launch_linear_widen(const moe_linear_desc& d, int M, int which, void
   const dim3 block(256);
   if (t.wparts == 3) {
     const dim3 grid = grid_for((size_t)d.N * t.pitch / 4, num_sms);
-    auto go = [&](auto kernel) { return launch_k(kernel, grid, block, 0, s, W, sc, (long long)d.K, d.N, d.K, t.pitch, out); };
+    auto go = [&](auto kernel) {
+      return launch_next(which == 0, kernel, grid, block, 0, s, W, sc, (long long)d.K, d.N, d.K, t.pitch, out);
+    };
     return d.wfmt == MOE_W_F32 ? go(linear_split_kernel<MOE_W_F32>)
                                : (d.wfmt == MOE_W_INT4_B32 ? go(linear_split_kernel<MOE_W_INT4_B32>)
                                                            : go(linear_split_kernel<MOE_W_INT4_B128>));
@@ -634,16 +645,16 @@ cudaError_t launch_linear_widen(const moe_linear_desc& d, int M, int which, void
   const size_t n16 = (size_t)d.N * d.K / 16;
   const dim3 grid = grid_for(n16, num_sms);
   switch (d.wfmt) {
-    case MOE_W_INT8_ROW: return launch_k(linear_widen_kernel<MOE_W_INT8_ROW>, grid, block, 0, s, W, sc, n16, d.K, out);
-    case MOE_W_INT4_B32: return launch_k(linear_widen_kernel<MOE_W_INT4_B32>, grid, block, 0, s, W, sc, n16, d.K, out);
-    default: return launch_k(linear_widen_kernel<MOE_W_INT4_B128>, grid, block, 0, s, W, sc, n16, d.K, out);
+    case MOE_W_INT8_ROW: return launch_next(which == 0, linear_widen_kernel<MOE_W_INT8_ROW>, grid, block, 0, s, W, sc, n16, d.K, out);
+    case MOE_W_INT4_B32: return launch_next(which == 0, linear_widen_kernel<MOE_W_INT4_B32>, grid, block, 0, s, W, sc, n16, d.K, out);
+    default: return launch_next(which == 0, linear_widen_kernel<MOE_W_INT4_B128>, grid, block, 0, s, W, sc, n16, d.K, out);
   }
 }
 
 cudaError_t launch_linear_split_x(const moe_linear_desc& d, const LinearArgs& a, void* workspace, int num_sms, cudaStream_t s) {
   const TcLayout t = tc_layout(d, a.M);
-  return launch_k(linear_split_kernel<MOE_W_F32>, grid_for((size_t)a.M * t.pitch / 4, num_sms), dim3(256), 0, s, a.x,
-                  static_cast<const float*>(nullptr), a.ldx, a.M, d.K, t.pitch,
+  return launch_next(!t.w_copy, linear_split_kernel<MOE_W_F32>, grid_for((size_t)a.M * t.pitch / 4, num_sms), dim3(256), 0, s, a.x,
+                     static_cast<const float*>(nullptr), a.ldx, a.M, d.K, t.pitch,
                   reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + t.x));
 }
 
@@ -684,14 +695,14 @@ cudaError_t launch_linear_tc(const moe_linear_desc& d, const LinearArgs& a, void
   if (e != cudaSuccess) return e;
   const long long tiles = (long long)t.mt * t.nt * t.splits;
   const int pairs = (int)std::min<long long>(tiles, num_sms / 2);
-  return launch_k(kernel, dim3(2 * pairs), dim3(kThreads), kSmem, s, mx, mw[0], mw[1], p, flags);
+  return launch_next(!t.w_copy && t.xparts == 1, kernel, dim3(2 * pairs), dim3(kThreads), kSmem, s, mx, mw[0], mw[1], p, flags);
 }
 
 bool linear_tc_split(const moe_linear_desc& d, int M) { return tc_layout(d, M).splits > 1; }
 
 cudaError_t launch_linear_sum(const moe_linear_desc& d, const LinearArgs& a, void* workspace, int num_sms, cudaStream_t s) {
   const TcLayout t = tc_layout(d, a.M);
-  return launch_k(linear_sum_kernel, grid_for((size_t)a.M * t.np / 4, num_sms), dim3(256), 0, s, tc_args(d, a, t, workspace));
+  return launch_next(false, linear_sum_kernel, grid_for((size_t)a.M * t.np / 4, num_sms), dim3(256), 0, s, tc_args(d, a, t, workspace));
 }
 
 }  // namespace moe
