@@ -419,6 +419,9 @@ template <int WF>
 struct Ring {
   using F = stream::Format<WF>;
   static constexpr bool kDigits = WF != MOE_W_BF16;       // gate/up products are integer ones
+  // Codes are up to 128 times what they stand for in units of the row's largest weight: h is kept
+  // smaller by a power of two, so that its products with codes overflow no sooner than h.
+  static constexpr float kHScale = WF == MOE_W_BF16 ? 1.f : 1.f / 256.f;
   static constexpr int kUpTiles = kDigits ? 2 : 1;        // token tiles of a gate/up unit
   static constexpr int kUpTokens = kDigits ? kUpTiles * stream::kDigitTokens : 8;
   static constexpr int kStage = 2 * (stream::kBoxBytes + F::kScaleBox);  // gate and up box, or down boxes
@@ -784,8 +787,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           if (2 * c + (k & 1) >= m) continue;
-          const float gate = sum[0][k] * (scale[0][k >> 1] * unit_x[k & 1]), up = sum[1][k] * (scale[1][k >> 1] * unit_x[k & 1]);
-          const float h = a.act == MOE_ACT_SILU ? silu_mul(gate, up) : gelu_tanh_mul(gate, up);
+          const float gate = sum[0][k] * unit_x[k & 1] * scale[0][k >> 1], up = sum[1][k] * unit_x[k & 1] * scale[1][k >> 1];
+          const float h = (a.act == MOE_ACT_SILU ? silu_mul(gate, up) : gelu_tanh_mul(gate, up)) * R::kHScale;
           const uint16_t hi = f32_to_bf16(h);
           const float rest = h - bf16_to_f32(hi);
           uint16_t* at = a.h2 + to[k & 1] + 8 * (k >> 1);
@@ -1033,7 +1036,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         if (j >= entry_n(now)) continue;
         const int p = sh.pair[shared ? 0 : entry_start(now) + j];
         const int to = shared ? entry_start(now) + j : p >> 9;
-        const float wt = (shared ? 1.f : sh.pair_w[p & 511]) * s_now;
+        const float wt = (shared ? 1.f : sh.pair_w[p & 511]) * s_now * (1.f / R::kHScale);
         sh.y[w][to][c < 2 ? g : g + 8] += wt * (c < 2 ? v[k] : v[2 + k]);
       }
       __syncwarp();

@@ -15,6 +15,7 @@ import torch
 import synth
 
 U = 2.0 ** -24
+TINY = 2.0 ** -126  # below the smallest normal number a product or a result loses its bits altogether
 HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
 STEPS = 16
 
@@ -66,6 +67,14 @@ def widened_error(wfmt, x_is_bf16, magnitude, exact_int4):
     return 0.0
 
 
+def digit_error(x, Wd, wfmt):
+    """bf16 tokens meet int8 and int4 weights as integers of 31 bits relative to the token's largest
+    value m: each column is off by at most half a unit, 2^(e - 31) with 2^e <= 2 m."""
+    if wfmt not in ("int8", "int4", "int4b128") or x.dtype != torch.bfloat16:
+        return 0.0
+    return 2.0 ** -30 * x.double().abs().amax(1, keepdim=True) * Wd.abs().sum(1)[None, :]
+
+
 def linear(x, W, s_b, up=None, act_name="none", residual=None, y_dtype=torch.float32, wfmt="f32", exact_int4=True):
     """(reference, bound) of y = act(W x + b) [* (W_up x + b_up)] + residual; W, W_up float64
     [N, K]; s_b, and up's second entry: fp64 biases or None."""
@@ -75,7 +84,7 @@ def linear(x, W, s_b, up=None, act_name="none", residual=None, y_dtype=torch.flo
     def product(Wd, b):
         v = xd @ Wd.T
         m = xd.abs() @ Wd.abs().T
-        e = sum_error(Wd.shape[1], m) + widened_error(wfmt, bf, m, exact_int4)
+        e = sum_error(Wd.shape[1], m) + widened_error(wfmt, bf, m, exact_int4) + digit_error(x, Wd, wfmt)
         if b is not None:
             v = v + b
             e = e + 2 * U * (v.abs() + b.abs())
@@ -91,7 +100,7 @@ def linear(x, W, s_b, up=None, act_name="none", residual=None, y_dtype=torch.flo
     if residual is not None:
         y = y + residual.double()
         e = e + 2 * U * (y.abs() + residual.double().abs())
-    return y, e + HALF[y_dtype] * (y.abs() + e)
+    return y, e + HALF[y_dtype] * (y.abs() + e) + TINY
 
 
 def route(x, W_r, b, mask, k, router, scale):
@@ -125,7 +134,7 @@ def ffn(x, gate, up, down, act_name):
     h = a * u
     ea = ACT_SLOPE * eg + STEPS * U * a.abs()
     eh = ea * u.abs() + a.abs() * eu + ea * eu
-    eh = eh + 2.0 ** -16 * (h.abs() + eh)  # kept to 16 significant bits at least
+    eh = eh + 2.0 ** -16 * (h.abs() + eh) + TINY  # kept to 16 significant bits at least
     y = h @ down.T
     e = eh @ down.abs().T + sum_error(down.shape[1], (h.abs() + eh) @ down.abs().T)
     return y, e
@@ -153,7 +162,7 @@ def few(x, idx, w, experts, act_name, shared=None, residual=None):
     if residual is not None:
         y, mag, terms = y + residual.double(), mag + residual.double().abs(), terms + 1
     e = e + sum_error(terms, mag + e)
-    return y, e + HALF[x.dtype] * (y.abs() + e)
+    return y, e + HALF[x.dtype] * (y.abs() + e) + TINY
 
 
 def check(got, ref, bound, what=""):

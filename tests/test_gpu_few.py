@@ -160,8 +160,9 @@ def test_fewer_selectable_experts_than_slots(active):
 
 
 @pytest.mark.flags
-def test_infinity_and_nan_stay_in_their_token():
-    layer = Layer()
+@pytest.mark.parametrize("wfmt", ["bf16", "int8", "int4"])
+def test_infinity_and_nan_stay_in_their_token(wfmt):
+    layer = Layer(wfmt=wfmt, shared=128)
     x = layer.x(4)
     clean = layer.dev.few(x.cuda())[0].clone()
     moe.moe_device_flags(clear=True)
@@ -171,6 +172,7 @@ def test_infinity_and_nan_stay_in_their_token():
     assert moe.moe_device_flags(clear=True) & moe.MOE_FLAG_NONFINITE_LOGIT
     assert bool((idx[[1, 3]] == -1).all()) and bool((w[[1, 3]] == 0).all())
     assert torch.equal(y[[0, 2]].view(torch.int16), clean[[0, 2]].view(torch.int16))
+    assert not bool(y[[1, 3]].isfinite().any())  # the shared expert still saw them
 
 
 @pytest.mark.flags
@@ -184,6 +186,49 @@ def test_nonfinite_weights_of_masked_and_unchosen_experts_do_not_matter():
             t[part][e] = float("nan") if n % 2 else float("inf")
     y2, idx2, _ = layer.dev.few(x.cuda())
     assert torch.equal(y2.view(torch.int16), y.view(torch.int16)) and torch.equal(idx2, idx)
+
+
+@pytest.mark.parametrize("wfmt", ["int8", "int4", "int4b128"])
+@pytest.mark.parametrize("scale", [1e-30, 1e-6, 1e6, 1e18])
+def test_tokens_of_any_magnitude(wfmt, scale):
+    """Digits are relative to the token's largest value: its magnitude does not matter."""
+    layer = Layer(wfmt=wfmt, bias=False)
+    x = (layer.x(3).float() * torch.tensor([1.0, scale, 0.0])[:, None]).to(torch.bfloat16)
+    y, idx, w = layer.dev.few(x.cuda())
+    layer.judge(x, y, idx, w)
+
+
+@pytest.mark.parametrize("wfmt", ["bf16", "int8", "int4"])
+def test_outliers_in_a_token(wfmt):
+    """A few columns thousands of times the others, as hidden states have them."""
+    layer = Layer(wfmt=wfmt, shared=128)
+    x = layer.x(5).float()
+    x[:, 7] *= 4000
+    x[1, 200] = -30000.0
+    x = x.to(torch.bfloat16)
+    y, idx, w = layer.dev.few(x.cuda())
+    layer.judge(x, y, idx, w)
+
+
+def test_beside_other_work():
+    """CTAs that cannot start because other work holds their SMs: their units are taken over,
+    and the results do not change."""
+    layer = Layer(E=64, k=8, H=1024, I=1024, wfmt="int8", shared=512)
+    xs = [layer.x(n, 60 + n).cuda() for n in (1, 4, 16)]
+    want = [[t.clone() for t in layer.dev.few(x)] for x in xs]
+    a = torch.randn(8192, 8192, device="cuda", dtype=torch.bfloat16)
+    busy, mine = torch.cuda.Stream(), [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(15):
+        with torch.cuda.stream(busy):
+            a @ a
+        for s in mine:
+            with torch.cuda.stream(s):
+                got += [(n, layer.dev.few(x)) for n, x in enumerate(xs)]
+    torch.cuda.synchronize()
+    for n, out in got:
+        assert all(torch.equal(p, q) for p, q in zip(out, want[n]))
 
 
 def test_large_activations_overflow_no_sooner_than_fp32():

@@ -91,10 +91,19 @@ def test_short_and_ragged_reductions(wfmt, xfmt, K, M):
 
 
 @pytest.mark.parametrize("wfmt", ["bf16", "int8", "int4", "int4b128"])
-@pytest.mark.parametrize("M", [1, 8, 48, 100, 500])
-def test_long_reductions(wfmt, M):
+@pytest.mark.parametrize("M", [1, 2, 8, 48, 100, 500])
+@pytest.mark.parametrize("yfmt", ["bf16", "f32"])
+def test_long_reductions(wfmt, M, yfmt):
     """Sums long enough to be split over several CTAs."""
-    Product(9216, 96, wfmt).run(M, residual=True)
+    Product(9216, 96, wfmt, yfmt=yfmt).run(M, residual=True)
+
+
+@pytest.mark.parametrize("wfmt,xfmt,gated", [("bf16", "bf16", False), ("bf16", "bf16", True), ("f32", "f32", False),
+                                             ("f32", "f32", True), ("int8", "f32", False), ("int4", "f32", False),
+                                             ("f32", "bf16", False)])
+def test_fp32_outputs_drained_in_segments(wfmt, xfmt, gated):
+    """Enough tiles that the reduction is not split, and columns for several segments."""
+    Product(1664, 2000, wfmt, xfmt, yfmt="f32", gated=gated, act="silu", bias=True).run(2500)
 
 
 @pytest.mark.parametrize("wfmt", ["bf16", "int8", "int4"])
@@ -127,10 +136,12 @@ def test_in_place_residual(M):
     assert torch.equal(y, r)
 
 
-@pytest.mark.parametrize("M", [1, 40, 200])
-def test_infinity_and_nan_stay_in_their_row(M):
-    p = Product(256, 96, "bf16")
+@pytest.mark.parametrize("wfmt", ["bf16", "int8", "int4"])
+@pytest.mark.parametrize("M", [0, 1, 4, 14, 40, 200])
+def test_infinity_and_nan_stay_in_their_row(M, wfmt):
+    p = Product(256, 96, wfmt)
     x = p.x(M + 2)
+    x[M:] = 1  # the same number of rows, so the same kernel
     clean = p.dev(x.cuda())
     x[M, 3], x[M + 1, 9] = float("nan"), float("inf")
     y = p.dev(x.cuda())
@@ -138,8 +149,29 @@ def test_infinity_and_nan_stay_in_their_row(M):
     assert bool(y[M].isnan().all()) and not bool(y[M + 1].isfinite().any())
 
 
+@pytest.mark.parametrize("wfmt", ["int8", "int4", "int4b128"])
+@pytest.mark.parametrize("scale", [1e-30, 1e-6, 1e6, 1e18])
+def test_tokens_of_any_magnitude(wfmt, scale):
+    """Digits are relative to the token's largest value: its magnitude does not matter."""
+    p = Product(512, 80, wfmt, yfmt="f32")
+    x = (p.x(2).float() * torch.tensor([scale, 0.0])[:, None]).to(torch.bfloat16)
+    p.judge(x, p.dev(x.cuda()))
+
+
 @pytest.mark.parametrize("wfmt,xfmt", [("bf16", "bf16"), ("int8", "bf16"), ("int4", "bf16"), ("f32", "f32")])
-@pytest.mark.parametrize("M", [4, 60, 300])
+@pytest.mark.parametrize("M", [2, 6, 18, 300])
+def test_outliers_in_a_row(wfmt, xfmt, M):
+    """A few columns thousands of times the others, as hidden states have them."""
+    p = Product(640, 75, wfmt, xfmt, bias=True)
+    x = p.x(M).float()
+    x[:, 7] *= 4000
+    x[0, 200] = -30000.0
+    x = x.to(p.x_dtype)
+    p.judge(x, p.dev(x.cuda()))
+
+
+@pytest.mark.parametrize("wfmt,xfmt", [("bf16", "bf16"), ("int8", "bf16"), ("int4", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("M", [2, 4, 60, 300])
 def test_same_call_same_bits_on_a_dirty_workspace(wfmt, xfmt, M):
     p = Product(1024, 272, wfmt, xfmt)
     x = p.x(M).cuda()
