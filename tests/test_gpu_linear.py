@@ -40,9 +40,9 @@ class Product:
         return torch.from_numpy(synth.normal_f32((M, self.N), seed, 9, 0.0, 1.0)).to(self.y_dtype)
 
     def judge(self, x, y, residual=None, what=""):
-        # int4 weights are widened exactly for up to 16 tokens; beyond, each is rounded to bf16 once,
-        # which is off by half a step of bf16 at most (moe_linear)
-        exact = x.shape[0] <= 16
+        # int4 weights are widened exactly for up to 16 tokens and for fp32 outputs; else each is rounded
+        # to bf16 once, which is off by half a step of bf16 at most (moe_linear)
+        exact = x.shape[0] <= 16 or self.y_dtype == torch.float32
         want, bound = ref.linear(x, self.W, self.b, None if self.Wu is None else (self.Wu, self.bu), self.act, residual,
                                  self.y_dtype, self.wfmt, exact)
         ref.check(y, want, bound, what)
@@ -68,9 +68,9 @@ def test_gated(wfmt, xfmt, M):
     Product(256, 136, wfmt, xfmt, act="gelu_tanh", gated=True, bias=M != 16).run(M, residual=M == 33)
 
 
-@pytest.mark.parametrize("wfmt", ["bf16", "int8", "int4", "f32"])
+@pytest.mark.parametrize("wfmt", ["bf16", "int8", "int4", "int4b128", "f32"])
 @pytest.mark.parametrize("yfmt", ["f32", "bf16"])
-@pytest.mark.parametrize("M", [3, 90])
+@pytest.mark.parametrize("M", [3, 20, 90])
 def test_output_formats(wfmt, yfmt, M):
     Product(256, 77, wfmt, "f32" if wfmt == "f32" else "bf16", yfmt=yfmt, bias=True).run(M, residual=True)
 
