@@ -803,7 +803,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     seek_up(at);
     // the lane's token columns: bf16, or a digit of each tile's token
     using Columns = std::conditional_t<R::kDigits, stream::Digits<WF>, stream::Bf16Columns<WF>>;
-    Columns x[R::kUpTiles], x_next[R::kUpTiles];
+    Columns x[R::kUpTiles] = {}, x_next[R::kUpTiles] = {};
     const char* tok[R::kUpTiles] = {};  // of the unit at `at`
     int tiles = 1, tiles_next = 1;
     size_t row = 0;                     // int4: row of the block scales

@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Walk at = {(int)blockIdx.x, w};
   seek(at);
   using Sum = std::conditional_t<DIG, stream::DigitSum<WF>, float>;
-  stream::Digits<WF> dx[DIG ? NT : 1], dx_next[DIG ? NT : 1];
+  stream::Digits<WF> dx[DIG ? NT : 1] = {}, dx_next[DIG ? NT : 1] = {};
   const int8_t* drow[DIG ? NT : 1];
   const float* units_x = p.units;
   auto fetch_digits = [&] {

@@ -107,10 +107,10 @@ struct Scales {
 };
 
 // int4 block scales of the lane's rows g and g + 8 for the four units of half h of a box
-template <int WF>
+template <int WF, bool BOXED>
 __device__ __forceinline__ void load_block_scales(const Scales& sc, int h, float (&s0)[4], float (&s8)[4]) {
   using F = Format<WF>;
-  if (F::kScaleBoxes && sc.in_box) {
+  if constexpr (BOXED) {
     const uint32_t at = sc.box + (lane_id() >> 2) * 32 + h * 16;
     const uint4 a = ld_shared_v4(at), b = ld_shared_v4(at + 256);
     s0[0] = __uint_as_float(a.x), s0[1] = __uint_as_float(a.y), s0[2] = __uint_as_float(a.z), s0[3] = __uint_as_float(a.w);
@@ -154,9 +154,9 @@ __device__ __forceinline__ void load_token(const uint16_t* tok, int left, uint4 
 // 4g + c works on rows g and g + 8.  A quad reads units {0, 2, 4, 6}, then {1, 3, 5, 7} of a row
 // (lane c: 2c and 2c + 1), so that the two rows of an eight-lane phase fall into different
 // banks; int4 lanes read word c of each unit.
-template <int WF, int MT>
-__device__ __forceinline__ void mac_box(uint32_t boxes, const uint4 (&x)[Format<WF>::kLoads], const Scales (&sc)[MT],
-                                        float (&acc)[MT][4]) {
+template <int WF, int MT, bool BOXED>
+__device__ __forceinline__ void mac_box_as(uint32_t boxes, const uint4 (&x)[Format<WF>::kLoads], const Scales (&sc)[MT],
+                                           float (&acc)[MT][4]) {
   using F = Format<WF>;
   const int g = lane_id() >> 2, c = lane_id() & 3;
   const uint32_t row = boxes + g * 128;
@@ -198,7 +198,7 @@ __device__ __forceinline__ void mac_box(uint32_t boxes, const uint4 (&x)[Format<
     for (int h = 0; h < 2; ++h) {
       float s0[MT][4], s8[MT][4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) load_block_scales<WF>(sc[mt], h, s0[mt], s8[mt]);
+      for (int mt = 0; mt < MT; ++mt) load_block_scales<WF, BOXED>(sc[mt], h, s0[mt], s8[mt]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint4 v = x[4 * h + i];
@@ -224,12 +224,22 @@ __device__ __forceinline__ void mac_box(uint32_t boxes, const uint4 (&x)[Format<
   }
 }
 
+// Where the scales are is asked once per box, here: a branch in the loop over the units would keep
+// the compiler from overlapping one unit's instructions with the next one's, and a unit is a
+// chain of some 80 cycles.
+template <int WF, int MT>
+__device__ __forceinline__ void mac_box(uint32_t boxes, const uint4 (&x)[Format<WF>::kLoads], const Scales (&sc)[MT],
+                                        float (&acc)[MT][4]) {
+  if (Format<WF>::kScaleBoxes && sc[0].in_box) mac_box_as<WF, MT, Format<WF>::kScaleBoxes>(boxes, x, sc, acc);
+  else mac_box_as<WF, MT, false>(boxes, x, sc, acc);
+}
+
 // The same for several tiles of 8 tokens: every code is widened once for all of them.  The token
 // columns are loaded here, piece by piece: load(nt, i) is the i-th 16-byte piece of the
 // lane's token of tile nt (in load_token's order).
-template <int WF, int MT, int NT, typename Load>
-__device__ __forceinline__ void mac_box_tiles(uint32_t boxes, int ntiles, Load load, const Scales (&sc)[MT],
-                                              float (&acc)[MT][NT][4]) {
+template <int WF, int MT, int NT, bool BOXED, typename Load>
+__device__ __forceinline__ void mac_box_tiles_as(uint32_t boxes, int ntiles, Load load, const Scales (&sc)[MT],
+                                                 float (&acc)[MT][NT][4]) {
   using F = Format<WF>;
   const int g = lane_id() >> 2, c = lane_id() & 3;
   const uint32_t row = boxes + g * 128;
@@ -275,7 +285,7 @@ __device__ __forceinline__ void mac_box_tiles(uint32_t boxes, int ntiles, Load l
     for (int h = 0; h < 2; ++h) {
       float s0[MT][4], s8[MT][4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) load_block_scales<WF>(sc[mt], h, s0[mt], s8[mt]);
+      for (int mt = 0; mt < MT; ++mt) load_block_scales<WF, BOXED>(sc[mt], h, s0[mt], s8[mt]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint4 x[NT];
@@ -312,6 +322,13 @@ __device__ __forceinline__ void mac_box_tiles(uint32_t boxes, int ntiles, Load l
       }
     }
   }
+}
+
+template <int WF, int MT, int NT, typename Load>
+__device__ __forceinline__ void mac_box_tiles(uint32_t boxes, int ntiles, Load load, const Scales (&sc)[MT],
+                                              float (&acc)[MT][NT][4]) {
+  if (Format<WF>::kScaleBoxes && sc[0].in_box) mac_box_tiles_as<WF, MT, NT, Format<WF>::kScaleBoxes>(boxes, ntiles, load, sc, acc);
+  else mac_box_tiles_as<WF, MT, NT, false>(boxes, ntiles, load, sc, acc);
 }
 
 // ---------------------------------------------------------------- tokens as digits
@@ -413,10 +430,10 @@ __device__ __forceinline__ void load_digits(const int8_t* row, Digits<WF>& x) {
 template <int WF>
 using DigitSum = std::conditional_t<Format<WF>::kInt4, float, int>;
 
-// acc[mt][nt] += box mt times the digits of tile nt < ntiles
-template <int WF, int MT, int NT>
-__device__ __forceinline__ void mac_box_digits(uint32_t boxes, int ntiles, const Digits<WF> (&x)[NT], const Scales (&sc)[MT],
-                                               DigitSum<WF> (&acc)[MT][NT][4]) {
+// acc[mt][nt] += box mt times the digits of tile nt < TILES
+template <int WF, int MT, int NT, int TILES, bool BOXED>
+__device__ __forceinline__ void mac_box_digits_as(uint32_t boxes, const Digits<WF> (&x)[NT], const Scales (&sc)[MT],
+                                                  DigitSum<WF> (&acc)[MT][NT][4]) {
   using F = Format<WF>;
   const int g = lane_id() >> 2, c = lane_id() & 3;
   const uint32_t row = boxes + g * 128;
@@ -428,8 +445,7 @@ __device__ __forceinline__ void mac_box_digits(uint32_t boxes, int ntiles, const
       for (int mt = 0; mt < MT; ++mt) {
         const uint4 a = ld_shared_v4(at + mt * kBoxBytes), b = ld_shared_v4(at + mt * kBoxBytes + 1024);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if (nt >= ntiles) break;
+        for (int nt = 0; nt < TILES; ++nt) {
           int(&d)[4] = acc[mt][nt];
           imma16832(d, a.x, b.x, a.y, b.y, x[nt].v[4 * h], x[nt].v[4 * h + 1], d[0], d[1], d[2], d[3]);
           imma16832(d, a.z, b.z, a.w, b.w, x[nt].v[4 * h + 2], x[nt].v[4 * h + 3], d[0], d[1], d[2], d[3]);
@@ -443,7 +459,7 @@ __device__ __forceinline__ void mac_box_digits(uint32_t boxes, int ntiles, const
     for (int h = 0; h < 2; ++h) {
       float s0[MT][4], s8[MT][4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) load_block_scales<WF>(sc[mt], h, s0[mt], s8[mt]);
+      for (int mt = 0; mt < MT; ++mt) load_block_scales<WF, BOXED>(sc[mt], h, s0[mt], s8[mt]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t at = row + (((4 * h + i) ^ g) << 4) + 4 * c;
@@ -454,8 +470,7 @@ __device__ __forceinline__ void mac_box_digits(uint32_t boxes, int ntiles, const
           const uint32_t al = (a << 4) & 0xF0F0F0F0u, ah = a & 0xF0F0F0F0u;
           const uint32_t bl = (b << 4) & 0xF0F0F0F0u, bh = b & 0xF0F0F0F0u;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if (nt >= ntiles) break;
+          for (int nt = 0; nt < TILES; ++nt) {
             int d[4];
             imma16832(d, al, bl, ah, bh, x[nt].v[8 * h + 2 * i], x[nt].v[8 * h + 2 * i + 1], kOne, kOne, kOne, kOne);
             acc[mt][nt][0] = fmaf(__int_as_float(d[0]) - 12582912.f, s0[mt][i], acc[mt][nt][0]);
@@ -466,6 +481,20 @@ __device__ __forceinline__ void mac_box_digits(uint32_t boxes, int ntiles, const
         }
       }
     }
+  }
+}
+
+// for ntiles tiles: one, or all of them (those without a token cost their instructions only)
+template <int WF, int MT, int NT>
+__device__ __forceinline__ void mac_box_digits(uint32_t boxes, int ntiles, const Digits<WF> (&x)[NT], const Scales (&sc)[MT],
+                                               DigitSum<WF> (&acc)[MT][NT][4]) {
+  constexpr bool kBoxes = Format<WF>::kScaleBoxes;
+  if (kBoxes && sc[0].in_box) {
+    if (ntiles == 1) mac_box_digits_as<WF, MT, NT, 1, kBoxes>(boxes, x, sc, acc);
+    else mac_box_digits_as<WF, MT, NT, NT, kBoxes>(boxes, x, sc, acc);
+  } else {
+    if (ntiles == 1) mac_box_digits_as<WF, MT, NT, 1, false>(boxes, x, sc, acc);
+    else mac_box_digits_as<WF, MT, NT, NT, false>(boxes, x, sc, acc);
   }
 }
 
