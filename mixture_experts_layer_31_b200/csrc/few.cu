@@ -457,7 +457,10 @@ struct StreamShared {
   uint32_t up[kMaxPairs + 4], down[kMaxPairs + 4];  // entries: shared first / shared last
   union alignas(16) {            // read in pieces of 16 bytes
     float part[2][kWarps][2][16][8];           // [unit parity][warp][gate, up][row][token]
-    float y[kWarps][MOE_FEW_MAX_TOKENS][16];   // down: each warp's share of 16 rows
+    struct {
+      float y[kWarps][MOE_FEW_MAX_TOKENS][16];   // down: each warp's share of 16 rows
+      uint32_t at[kMaxPairs + 4][kDownTokens];   // by down entry: where its tokens' h starts
+    };
     struct {
       int e[kMaxPairs];                        // building the plan: by pair
       int by_rank[kMaxPairs];                  // in expert order: expert, -1 at the end
@@ -534,9 +537,6 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   struct UpWalk {
     int n, entry, block, j;  // the team's n-th unit: entry and block of rows; box
   };
-  struct DownWalk {
-    int blk, x, i;  // block of y's rows, entry, stage
-  };
   int n_up = su, n_down = 0;  // entries; without the routed ones before the plan
   auto step_unit = [&](UpWalk& k) {
     ++k.n;
@@ -554,34 +554,43 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       step_unit(k);
     }
   };
-  auto seek_down = [&](DownWalk& k) {
-    for (;;) {
-      if (k.x >= n_down) {
-        k.blk += grid;
-        k.x = down_team, k.i = down_w;
-        if (k.blk >= hb || k.x >= n_down) {
-          k.blk = hb;
-          return;
-        }
-      }
-      const int steps = k.x < n_down - sd ? steps_r : steps_s;
-      if (k.i < steps) return;
-      k.i -= steps;
-      k.x += down_teams;
-    }
+  // The boxes of a team's down entries, one after the other, go round its warps too; the list's
+  // blocks of y's rows follow one another.  Which entry and stage of it a warp's n-th stage is
+  // takes two divisions, so a lane works it out for one stage of the next 32: those of
+  // number n with n % 32 == lane.
+  int per_blk = 0, down_blk = hb, n_stages = 0;  // a warp's stages of one block; the list's first block; its stages
+  int entries_r = 0;                             // the team's routed entries; those of the shared expert follow
+  uint32_t win = 0;                              // entry << 16 | stage of the entry
+  int win_blk = 0;
+  auto window = [&](int from) {
+    if (n_stages == 0) return;
+    const uint32_t n = (uint32_t)from + ((uint32_t)(lane - from) & 31u), q = n / (uint32_t)per_blk;
+    int box = down_w + (int)(n - q * (uint32_t)per_blk) * a.down_team, x = 0, steps = steps_r;
+    if (box >= entries_r * steps_r) box -= entries_r * steps_r, x = entries_r, steps = steps_s;
+    const int of = box / steps;
+    win = (uint32_t)(down_team + (x + of) * down_teams) << 16 | (uint32_t)(box - of * steps);
+    win_blk = down_blk + (int)q * grid;
   };
   auto first_down = [&](int list) {
-    DownWalk k = {list - grid, n_down, 0};
-    seek_down(k);
-    return k;
+    auto of_team = [&](int n) { return n > down_team ? (n - down_team + down_teams - 1) / down_teams : 0; };
+    const int entries = of_team(n_down);
+    entries_r = of_team(n_down - sd);
+    const int boxes = entries_r * steps_r + (entries - entries_r) * steps_s;
+    per_blk = boxes > down_w ? (boxes - down_w + a.down_team - 1) / a.down_team : 0;
+    down_blk = list;
+    n_stages = list < hb ? per_blk * ((hb - list + grid - 1) / grid) : 0;
+    window(0);
   };
 
   // copies run kStages ahead: `head` and `head_down` are the next to start
   int issued = 0, in_slot = 0;
   UpWalk head = first_unit((int)blockIdx.x, up_w);
   seek_up(head);
-  DownWalk head_down = {hb, 0, 0};
+  int head_down = 0;
   auto issue = [&](bool down) {
+    uint32_t v = 0;
+    int blk = 0;
+    if (down) v = __shfl_sync(0xFFFFFFFFu, win, head_down & 31), blk = __shfl_sync(0xFFFFFFFFu, win_blk, head_down & 31);
     if (lane == 0 && !dead) {
       uint8_t* stage = ring + in_slot * R::kStage;
       uint64_t* bar = &sh.full[w][in_slot];
@@ -599,10 +608,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           tma_load_2d(stage + 2 * stream::kBoxBytes + F::kScaleBox, sm + 1, head.j * 8, row, bar);
         }
       } else {
-        const uint32_t e = entry_e(sh.down[head_down.x]);
+        const uint32_t e = entry_e(sh.down[v >> 16]);
         const bool shared = e == kSharedEntry;
-        const int row = head_down.blk * 16 + (shared ? 0 : (int)e * a.H);
-        const int j = head_down.i * R::kDownBoxes;
+        const int row = blk * 16 + (shared ? 0 : (int)e * a.H);
+        const int j = (int)(v & 0xFFFFu) * R::kDownBoxes;
         const int n = min((shared ? boxes_s : boxes_i) - j, R::kDownBoxes);
         const bool boxed = F::kScaleBoxes && a.boxed[shared ? 3 : 1];
         const CUtensorMap* wm = shared ? maps.ws + 2 : maps.w + 2;
@@ -623,10 +632,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   auto issue_next = [&] {
     if (head.entry < n_up) {
       issue_up();
-    } else if (head_down.blk < hb) {
+    } else if (head_down < n_stages) {
       issue(true);
-      head_down.i += a.down_team;
-      seek_down(head_down);
+      ++head_down;
     }
   };
   // The shared expert's units need no routing, and weights are nothing that the launch before this
@@ -687,7 +695,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   // the usual case: every CTA has started, so no list will be left over, and the rings may run on
   // into the down weights
   const bool all = sh.all != 0;
-  if (all) head_down = first_down((int)blockIdx.x);
+  if (all) first_down((int)blockIdx.x);
   auto fill = [&](int have) {
 #pragma unroll 1
     for (int i = have; i < R::kStages; ++i) issue_next();
@@ -701,8 +709,6 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   static_assert(MOE_FEW_MAX_TOKENS <= 2 * kWarps, "a warp has at most two tokens' weights");
   __syncthreads();
 
-  const uint16_t* hr = a.h2;                      // h of the routed pairs, [P, I]
-  const uint16_t* hs = a.h2 + (size_t)P * a.I;    // h of the shared expert, [T, Is]
   int done = 0, out_slot = 0;                     // stages read
   uint32_t phase = 0;
   auto landed = [&] {
@@ -923,6 +929,12 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     return;
   }
   for (int i = threadIdx.x; i < kWarps * MOE_FEW_MAX_TOKENS * 16; i += kStreamThreads) (&sh.y[0][0][0])[i] = 0.f;
+  for (int i = threadIdx.x; i < n_down * kDownTokens; i += kStreamThreads) {
+    const uint32_t en = sh.down[i / kDownTokens];
+    const int j = entry_start(en) + min(i % kDownTokens, entry_n(en) - 1);  // columns past the tokens are not used
+    sh.at[i / kDownTokens][i % kDownTokens] =
+        entry_e(en) == kSharedEntry ? (uint32_t)P * a.I + (uint32_t)j * a.Is : (uint32_t)(sh.pair[j] & 511) * a.I;
+  }
   if (threadIdx.x == 0) {
     __threadfence();
     atomicAdd(&a.counters[kFewDone], (uint32_t)n_lists);
@@ -943,119 +955,114 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 
   // ---------------------------------------------------------------- down and combine
   constexpr int DB = R::kDownBoxes;
-  uint4 x_next[DB][F::kLoads];
-  DownWalk at;
-  // of the entry at `at`: its tokens, reduction length, the lane's token (value or remainder)
-  uint32_t en = 0;
+  uint4 x[DB][F::kLoads];
+  // the warp's next stage: of which entry and where in it; the entry's reduction length, the lane's
+  // token (value or remainder)
+  uint32_t stage_at = 0, en = 0;
   int K = 0;
-  const uint16_t* tok = nullptr;
+  const uint16_t* const h_lane = a.h2 + (g < 4 ? 0 : a.plane);
   float s_row = 1.f;      // int8: scale of the row whose sums the lane will hold
-  const float* s0 = nullptr;  // int4: block scales of row g
-  auto entry_of = [&] {
-    en = sh.down[at.x];
+  const float* s0 = nullptr;  // int4, scales not copied: block scales of row g
+  bool boxed = false;
+  auto fetch = [&](int n) {
+    stage_at = __shfl_sync(0xFFFFFFFFu, win, n & 31);
+    const int blk = __shfl_sync(0xFFFFFFFFu, win_blk, n & 31);
+    en = sh.down[stage_at >> 16];
     const bool shared = entry_e(en) == kSharedEntry;
-    const size_t row = (shared ? 0 : (size_t)entry_e(en) * a.H) + at.blk * 16 + g;
-    const int j = entry_start(en) + min(g & 3, entry_n(en) - 1);  // columns past the tokens are not used
     K = shared ? a.Is : a.I;
-    tok = (shared ? hs + (size_t)j * a.Is : hr + (size_t)(sh.pair[j] & 511) * a.I) + (g < 4 ? 0 : a.plane);
-    if constexpr (WF == MOE_W_INT8_ROW) s_row = __ldg((shared ? a.ss[2] : a.s[2]) + row + (c < 2 ? 0 : 8));
-    if constexpr (F::kInt4) s0 = (shared ? a.ss[2] : a.s[2]) + row * (size_t)(K >> F::kScaleShift);
-  };
-  auto fetch = [&] {
-    const int c0 = at.i * DB * F::kBoxCols, left = K - c0;
+    boxed = F::kScaleBoxes && a.boxed[shared ? 3 : 1];
+    const int c0 = (int)(stage_at & 0xFFFFu) * DB * F::kBoxCols, left = K - c0;
+    const uint16_t* tok = h_lane + (sh.at[stage_at >> 16][g & 3] + c0);
 #pragma unroll
     for (int d = 0; d < DB; ++d)
       if (d == 0 || left > d * F::kBoxCols)
-        stream::load_token<WF>(tok + c0 + d * F::kBoxCols, left - d * F::kBoxCols, x_next[d]);
+        stream::load_token<WF>(tok + d * F::kBoxCols, left - d * F::kBoxCols, x[d]);
+    if constexpr (WF == MOE_W_INT8_ROW) {
+      const int row = (shared ? 0 : (int)entry_e(en) * a.H) + blk * 16 + g;
+      s_row = __ldg((shared ? a.ss[2] : a.s[2]) + row + (c < 2 ? 0 : 8));
+    }
+    if constexpr (F::kInt4) {
+      if (!boxed) {
+        const size_t row = (shared ? 0 : (size_t)entry_e(en) * a.H) + blk * 16 + g;
+        s0 = (shared ? a.ss[2] : a.s[2]) + row * (size_t)(K >> F::kScaleShift);
+      }
+    }
   };
 #pragma unroll 1
   for (int i = 0; i < n_lists; ++i) {
-  at = first_down(sh.lists[i]);
-  if (!all || i > 0) {
-    head_down = at;
-    fill(0);
-  }
-  if (at.blk < hb) {
-    entry_of();
-    fetch();
-  }
-  for (int blk = sh.lists[i]; blk < hb; blk += grid) {
-    float acc[1][4] = {};
+    if (!all || i > 0) {
+      first_down(sh.lists[i]);
+      head_down = 0;
+      fill(0);
+    }
+    if (n_stages > 0) fetch(0);
+    int n = 0;
+    for (int blk = sh.lists[i]; blk < hb; blk += grid) {
+      float acc[1][4] = {};
 #pragma unroll 1
-    while (at.blk == blk) {
-      uint4 x[DB][F::kLoads];
+      for (int r = 0; r < per_blk; ++r) {
+        const uint32_t stage = smem_u32(ring + out_slot * R::kStage);
+        const int c0 = (int)(stage_at & 0xFFFFu) * DB * F::kBoxCols, left = K - c0;
+        stream::Scales sc[DB][1];
+        if constexpr (F::kInt4) {
 #pragma unroll
-      for (int d = 0; d < DB; ++d)
-#pragma unroll
-        for (int i = 0; i < F::kLoads; ++i) x[d][i] = x_next[d][i];
-      const uint32_t stage = smem_u32(ring + out_slot * R::kStage);
-      const int c0 = at.i * DB * F::kBoxCols, left = K - c0;
-      stream::Scales sc[DB][1];
-      if constexpr (F::kInt4) {
-#pragma unroll
-        for (int d = 0; d < DB; ++d) {
-          sc[d][0].box = stage + 2 * stream::kBoxBytes + d * F::kScaleBox;
-          sc[d][0].in_box = a.boxed[entry_e(en) == kSharedEntry ? 3 : 1];
-          sc[d][0].left = left - d * F::kBoxCols;
-          if (!sc[d][0].in_box) {
-            sc[d][0].s0 = s0 + (c0 + d * F::kBoxCols >> F::kScaleShift);
-            sc[d][0].s8 = sc[d][0].s0 + 8 * (size_t)(K >> F::kScaleShift);
+          for (int d = 0; d < DB; ++d) {
+            sc[d][0].box = stage + 2 * stream::kBoxBytes + d * F::kScaleBox;
+            sc[d][0].in_box = boxed;
+            sc[d][0].left = left - d * F::kBoxCols;
+            if (!boxed) {
+              sc[d][0].s0 = s0 + (c0 + d * F::kBoxCols >> F::kScaleShift);
+              sc[d][0].s8 = sc[d][0].s0 + 8 * (size_t)(K >> F::kScaleShift);
+            }
           }
         }
-      }
-      // the next stage's tokens, of the same entry or of the next
-      const uint32_t now = en;
-      const float s_now = s_row;
-      const int x_now = at.x;
-      at.i += a.down_team;
-      seek_down(at);
-      const bool last = at.x != x_now || at.blk != blk;
-      if (at.blk < hb) {
-        if (last) entry_of();
-        fetch();
-      }
-      landed();
+        landed();
 #pragma unroll
-      for (int d = 0; d < DB; ++d) {
-        if (d > 0 && left <= d * F::kBoxCols) break;
-        stream::mac_box<WF, 1>(stage + d * stream::kBoxBytes, x[d], sc[d], acc);
-      }
-      read();
-      if (!last) continue;
-      // the entry's sums, weighted, to this warp's share of y
-      const bool shared = entry_e(now) == kSharedEntry;
-      float v[4];
+        for (int d = 0; d < DB; ++d) {
+          if (d > 0 && left <= d * F::kBoxCols) break;
+          stream::mac_box<WF, 1>(stage + d * stream::kBoxBytes, x[d], sc[d], acc);
+        }
+        // the next stage's tokens, of the same entry or of the next
+        const uint32_t now = en, x_now = stage_at >> 16;
+        const float s_now = s_row;
+        if ((++n & 15) == 0) window(n);
+        if (n < n_stages) fetch(n);
+        read();
+        if (r + 1 < per_blk && stage_at >> 16 == x_now) continue;
+        // the entry's sums, weighted, to this warp's share of y
+        const bool shared = entry_e(now) == kSharedEntry;
+        float v[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[k] = acc[0][k] + __shfl_xor_sync(0xFFFFFFFFu, acc[0][k], 2);
-        acc[0][k] = 0.f;
-      }
+        for (int k = 0; k < 4; ++k) {
+          v[k] = acc[0][k] + __shfl_xor_sync(0xFFFFFFFFu, acc[0][k], 2);
+          acc[0][k] = 0.f;
+        }
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int j = 2 * (c & 1) + k;
-        if (j >= entry_n(now)) continue;
-        const int p = sh.pair[shared ? 0 : entry_start(now) + j];
-        const int to = shared ? entry_start(now) + j : p >> 9;
-        const float wt = (shared ? 1.f : sh.pair_w[p & 511]) * s_now * (1.f / R::kHScale);
-        sh.y[w][to][c < 2 ? g : g + 8] += wt * (c < 2 ? v[k] : v[2 + k]);
+        for (int k = 0; k < 2; ++k) {
+          const int j = 2 * (c & 1) + k;
+          if (j >= entry_n(now)) continue;
+          const int p = sh.pair[shared ? 0 : entry_start(now) + j];
+          const int to = shared ? entry_start(now) + j : p >> 9;
+          const float wt = (shared ? 1.f : sh.pair_w[p & 511]) * s_now * (1.f / R::kHScale);
+          sh.y[w][to][c < 2 ? g : g + 8] += wt * (c < 2 ? v[k] : v[2 + k]);
+        }
+        __syncwarp();
       }
-      __syncwarp();
+      __syncthreads();
+      for (int i = threadIdx.x; i < a.T * 16; i += kStreamThreads) {
+        const int t = i >> 4, r = i & 15;
+        const size_t to = (size_t)t * a.H + blk * 16 + r;
+        float y = 0.f;
+#pragma unroll
+        for (int s = 0; s < kWarps; ++s) {
+          y += sh.y[s][t][r];
+          sh.y[s][t][r] = 0.f;
+        }
+        if (a.residual) y += bf16_to_f32(static_cast<const uint16_t*>(a.residual)[to]);
+        static_cast<uint16_t*>(a.y)[to] = f32_to_bf16(y);
+      }
+      __syncthreads();
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < a.T * 16; i += kStreamThreads) {
-      const int t = i >> 4, r = i & 15;
-      const size_t to = (size_t)t * a.H + blk * 16 + r;
-      float y = 0.f;
-#pragma unroll
-      for (int s = 0; s < kWarps; ++s) {
-        y += sh.y[s][t][r];
-        sh.y[s][t][r] = 0.f;
-      }
-      if (a.residual) y += bf16_to_f32(static_cast<const uint16_t*>(a.residual)[to]);
-      static_cast<uint16_t*>(a.y)[to] = f32_to_bf16(y);
-    }
-    __syncthreads();
-  }
   }
   // after a wait that ran out: leave only when the copies have landed
   if (dead) {
