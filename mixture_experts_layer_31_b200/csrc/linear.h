@@ -19,11 +19,19 @@ struct LinearArgs {
 };
 
 // Up to this many bf16 tokens the weights stream through warp-wide matrix instructions; beyond, the
-// tensor cores take them, quantised ones after a pass that widens them.  Measured, stream and
-// tensor cores: bf16 9216 x 2304, 32 tokens 23 and 22 us, 64 tokens 42 and 25; int8, the same
-// shape, 64 tokens 36 and 42; int4 2048 x 4999, 17 tokens 25 and 25, 32 tokens 31 and 26.
-inline int linear_stream_tokens(int wfmt) {
-  return wfmt == MOE_W_BF16 ? 32 : (wfmt == MOE_W_INT8_ROW ? 64 : 16);
+// tensor cores take them, quantised ones after a pass that widens them.  The stream costs more
+// for every tile of 8 tokens, the more so the more weights there are; the tensor cores have a
+// fixed cost of some 17 us (two launches, few units) and the widening pass.  Measured, stream and
+// tensor cores, in us:
+//   bf16   9216 x 2304, 32 tokens 17, 20;  2304 x 18432, 24 tokens 30, 29, 32 tokens 34, 24
+//   int8   9216 x 2304, 64 tokens 29, 37;  2304 x (9216 + 9216), 48 tokens 49, 52, 64 tokens 62, 54
+//   int4   2304 x (9216 + 9216), 40 tokens 46, 52;  2048 x 4999, 32 tokens 15, 23, 48 tokens 25, 23;
+//          9216 x 2304, 48 tokens 25, 36, 64 tokens 40, 38
+inline int linear_stream_tokens(const moe_linear_desc& d) {
+  const bool large = (int64_t)d.N * d.K * (d.W_up ? 2 : 1) > 32 << 20;
+  if (d.wfmt == MOE_W_INT8_ROW) return large ? 48 : 64;
+  if (d.wfmt == MOE_W_BF16) return large ? 24 : 32;
+  return d.K > 4096 ? 48 : 40;
 }
 
 __device__ __forceinline__ float linear_act(float v, int act) {

@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint16_t* t = x + (size_t)min(nt * 8 + g, a.M - 1) * a.ldx + c0;
           return col < left ? *reinterpret_cast<const uint4*>(t + col) : make_uint4(0, 0, 0, 0);
         };
-        stream::mac_box_tiles<WF, MT, NT>(stage, ntiles, load, sc, acc);
+        stream::mac_box_tiles<WF, MT, NT>(stage, load, sc, acc);
       }
       __syncwarp();
       ++done;
@@ -332,21 +332,27 @@ cudaError_t launch(const moe_linear_desc& d, const LinearArgs& a, void* ws, int 
     if (a.M <= 8)
       return two ? launch<WF, 2, 1, false>(d, a, ws, num_sms, flags, s) : launch<WF, 1, 1, false>(d, a, ws, num_sms, flags, s);
   }
-  if (a.M <= 16)
-    return two ? launch<WF, 2, 2, false>(d, a, ws, num_sms, flags, s) : launch<WF, 1, 2, false>(d, a, ws, num_sms, flags, s);
-  if constexpr (WF != MOE_W_INT4_B32 && WF != MOE_W_INT4_B128) {
-    if (a.M <= 32)
-      return two ? launch<WF, 2, 4, false>(d, a, ws, num_sms, flags, s) : launch<WF, 1, 4, false>(d, a, ws, num_sms, flags, s);
+  auto run = [&](auto tiles) {
+    constexpr int NT = decltype(tiles)::value;
+    return two ? launch<WF, 2, NT, false>(d, a, ws, num_sms, flags, s) : launch<WF, 1, NT, false>(d, a, ws, num_sms, flags, s);
+  };
+  using std::integral_constant;
+  if (a.M <= 16) return run(integral_constant<int, 2>());
+  if (a.M <= 24) return run(integral_constant<int, 3>());
+  if (a.M <= 32) return run(integral_constant<int, 4>());
+  if constexpr (WF != MOE_W_BF16) {
+    if (a.M <= 40) return run(integral_constant<int, 5>());
+    if (a.M <= 48) return run(integral_constant<int, 6>());
   }
   if constexpr (WF == MOE_W_INT8_ROW)
-    return two ? launch<WF, 2, 8, false>(d, a, ws, num_sms, flags, s) : launch<WF, 1, 8, false>(d, a, ws, num_sms, flags, s);
+    if (a.M <= 64) return run(integral_constant<int, 8>());
   return cudaErrorInvalidValue;  // not reached: linear_stream_tokens()
 }
 
 }  // namespace
 
 bool linear_stream_ok(const moe_linear_desc& d, int M) {
-  return d.xfmt == MOE_X_BF16 && d.wfmt != MOE_W_F32 && M <= linear_stream_tokens(d.wfmt);
+  return d.xfmt == MOE_X_BF16 && d.wfmt != MOE_W_F32 && M <= linear_stream_tokens(d);
 }
 
 bool linear_stream_digits(const moe_linear_desc& d, int M) {

@@ -611,7 +611,7 @@ TcLayout tc_layout(const moe_linear_desc& d, int M) {
 
 bool linear_tc_ok(const moe_linear_desc& d, int M) {
   const bool f32 = d.xfmt == MOE_X_F32 || d.wfmt == MOE_W_F32;
-  return M > (f32 ? kLinearRowTokens : linear_stream_tokens(d.wfmt));
+  return M > (f32 ? kLinearRowTokens : linear_stream_tokens(d));
 }
 
 size_t linear_tc_workspace(const moe_linear_desc& d, int M) { return tc_layout(d, M).total; }

@@ -81,6 +81,16 @@ __device__ __forceinline__ uint32_t widen_int4(uint32_t w, int j) {
   return and_xor(v, 0x00780078u, 0x41C041C0u);
 }
 
+// the same columns as a bf16 pair of q itself: (16 + low 3 bits) - (16 or 24 by the sign bit)
+__device__ __forceinline__ uint32_t widen_int4_signed(uint32_t w, int j) {
+  const uint32_t v = j == 0 ? w << 3 : w >> (4 * j - 3);
+  uint32_t r;
+  asm("add.rn.bf16x2 %0, %1, %2;"
+      : "=r"(r)
+      : "r"(and_or(v, 0x00380038u, 0x41804180u)), "r"(and_or(v, 0x00400040u, 0xC180C180u)));
+  return r;
+}
+
 template <int WF>
 struct Format {
   static constexpr bool kInt4 = WF == MOE_W_INT4_B32 || WF == MOE_W_INT4_B128;
@@ -234,11 +244,12 @@ __device__ __forceinline__ void mac_box(uint32_t boxes, const uint4 (&x)[Format<
   else mac_box_as<WF, MT, false>(boxes, x, sc, acc);
 }
 
-// The same for several tiles of 8 tokens: every code is widened once for all of them.  The token
-// columns are loaded here, piece by piece: load(nt, i) is the i-th 16-byte piece of the
-// lane's token of tile nt (in load_token's order).
+// The same for several tiles of 8 tokens: every code is widened once for all of them, int4 with its
+// sign, as the products with -24 would be needed for every tile.  The token columns are loaded
+// here, piece by piece: load(nt, i) is the i-th 16-byte piece of the lane's token of tile nt (in
+// load_token's order).  No branch on the number of tiles keeps a later unit's loads back.
 template <int WF, int MT, int NT, bool BOXED, typename Load>
-__device__ __forceinline__ void mac_box_tiles_as(uint32_t boxes, int ntiles, Load load, const Scales (&sc)[MT],
+__device__ __forceinline__ void mac_box_tiles_as(uint32_t boxes, Load load, const Scales (&sc)[MT],
                                                  float (&acc)[MT][NT][4]) {
   using F = Format<WF>;
   const int g = lane_id() >> 2, c = lane_id() & 3;
@@ -252,7 +263,7 @@ __device__ __forceinline__ void mac_box_tiles_as(uint32_t boxes, int ntiles, Loa
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < kHalf; ++i)
-          if (nt < ntiles) x[nt][i] = load(nt, h * kHalf + i);
+          x[nt][i] = load(nt, h * kHalf + i);
       const uint32_t at = row + (((2 * c + h) ^ g) << 4);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
@@ -260,7 +271,6 @@ __device__ __forceinline__ void mac_box_tiles_as(uint32_t boxes, int ntiles, Loa
         if constexpr (WF == MOE_W_BF16) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            if (nt >= ntiles) break;
             mma16816(acc[mt][nt], av.x, bv.x, av.y, bv.y, x[nt][0].x, x[nt][0].y);
             mma16816(acc[mt][nt], av.z, bv.z, av.w, bv.w, x[nt][0].z, x[nt][0].w);
           }
@@ -271,8 +281,7 @@ __device__ __forceinline__ void mac_box_tiles_as(uint32_t boxes, int ntiles, Loa
             const uint32_t a0 = widen_int8(a[i]), a1 = widen_int8(b[i]), a2 = widen_int8(a[i] >> 8), a3 = widen_int8(b[i] >> 8);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              if (nt >= ntiles) break;
-              const uint4 v = x[nt][i >> 1];
+                const uint4 v = x[nt][i >> 1];
               const uint32_t lo = (i & 1) ? v.z : v.x, hi = (i & 1) ? v.w : v.y;
               mma16816(acc[mt][nt], a0, a1, a2, a3, __byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
             }
@@ -291,27 +300,23 @@ __device__ __forceinline__ void mac_box_tiles_as(uint32_t boxes, int ntiles, Loa
         uint4 x[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-          if (nt < ntiles) x[nt] = load(nt, 4 * h + i);
+          x[nt] = load(nt, 4 * h + i);
         const uint32_t at = row + (((4 * h + i) ^ g) << 4) + 4 * c;
         uint32_t wa[MT][4], wb[MT][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           const uint32_t a = ld_shared_u32(at + mt * kBoxBytes), b = ld_shared_u32(at + mt * kBoxBytes + 1024);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) wa[mt][k] = widen_int4(a, k), wb[mt][k] = widen_int4(b, k);
+          for (int k = 0; k < 4; ++k) wa[mt][k] = widen_int4_signed(a, k), wb[mt][k] = widen_int4_signed(b, k);
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          if (nt >= ntiles) break;
           const uint32_t b0 = __byte_perm(x[nt].x, x[nt].z, 0x5410), b1 = __byte_perm(x[nt].x, x[nt].z, 0x7632);
           const uint32_t b2 = __byte_perm(x[nt].y, x[nt].w, 0x5410), b3 = __byte_perm(x[nt].y, x[nt].w, 0x7632);
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
-          mma16816(d, kMinus24, kMinus24, kMinus24, kMinus24, b0, b1);
-          mma16816(d, kMinus24, kMinus24, kMinus24, kMinus24, b2, b3);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            float q[4];
-            mma16816(q, wa[mt][0], wb[mt][0], wa[mt][1], wb[mt][1], b0, b1, d);
+            float q[4] = {0.f, 0.f, 0.f, 0.f};
+            mma16816(q, wa[mt][0], wb[mt][0], wa[mt][1], wb[mt][1], b0, b1);
             mma16816(q, wa[mt][2], wb[mt][2], wa[mt][3], wb[mt][3], b2, b3);
             acc[mt][nt][0] = fmaf(q[0], s0[mt][i], acc[mt][nt][0]);
             acc[mt][nt][1] = fmaf(q[1], s0[mt][i], acc[mt][nt][1]);
@@ -325,10 +330,10 @@ __device__ __forceinline__ void mac_box_tiles_as(uint32_t boxes, int ntiles, Loa
 }
 
 template <int WF, int MT, int NT, typename Load>
-__device__ __forceinline__ void mac_box_tiles(uint32_t boxes, int ntiles, Load load, const Scales (&sc)[MT],
+__device__ __forceinline__ void mac_box_tiles(uint32_t boxes, Load load, const Scales (&sc)[MT],
                                               float (&acc)[MT][NT][4]) {
-  if (Format<WF>::kScaleBoxes && sc[0].in_box) mac_box_tiles_as<WF, MT, NT, Format<WF>::kScaleBoxes>(boxes, ntiles, load, sc, acc);
-  else mac_box_tiles_as<WF, MT, NT, false>(boxes, ntiles, load, sc, acc);
+  if (Format<WF>::kScaleBoxes && sc[0].in_box) mac_box_tiles_as<WF, MT, NT, Format<WF>::kScaleBoxes>(boxes, load, sc, acc);
+  else mac_box_tiles_as<WF, MT, NT, false>(boxes, load, sc, acc);
 }
 
 // ---------------------------------------------------------------- tokens as digits
