@@ -279,6 +279,9 @@ MOE_API moe_status moe_forward_block(const moe_desc* d, const moe_shared_expert*
  *   - sums in fp32, one rounding to y's format.  The activations between the projections
  *     are kept to at least 16 significant bits.  Results do not depend on timing: the same
  *     call gives the same bits.
+ *   - bf16 tokens meet int8 and int4 gate and up weights as integers of 31 bits relative to the
+ *     token's largest magnitude: what lies 22 binary places and more below that loses low
+ *     bits, and a token that holds an infinity or NaN gives NaN in its whole row of y.
  *   - d->path is not read.
  * The workspace (moe_few_workspace_size bytes, 256-byte aligned) needs no initial state;
  * calls on one stream may share it, calls that can overlap must not.  Asynchronous on
@@ -315,6 +318,12 @@ MOE_API moe_status moe_few_forward(const moe_desc* d, const moe_shared_expert* s
  *   to their element.  y may be residual itself (same ldr and ldy; each element is read before
  *   it is written, by the same thread) and must not overlap x.  M = 0 does nothing.
  *   Columns between N and ldy, and what lies behind the last row, are not touched.
+ * Sums are fp32 (integers where a few bf16 tokens meet int8 or int4 weights: the token is
+ * taken as integers of 31 bits relative to its largest magnitude, and one that holds an
+ * infinity or NaN gives NaN in its whole row of y).  fp32 weights and tokens are multiplied in
+ * fp32, for more tokens in three bf16 parts each that hold every bit.  int4 weights are
+ * exact for up to 40 tokens (of bf16; 48 where K > 4096) and wherever y is fp32; beyond, with
+ * bf16 tokens and bf16 y, each is rounded to bf16 once.
  * The workspace is as for moe_forward: moe_linear_workspace_size bytes (may be 0, then it
  * may be NULL), 256-byte aligned, no initial state needed, shared by the calls of one
  * stream only.  Asynchronous on `stream`, no allocation, capturable.

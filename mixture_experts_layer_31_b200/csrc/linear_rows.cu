@@ -1,7 +1,9 @@
 // The dense product in fp32 multiply-adds for a few tokens, where tokens or weights are fp32:
 // a warp takes R rows of W, its lanes 8 columns in turn, for TT tokens at a time.  The
 // weights' way from HBM bounds it; R rows share a token's columns, without which the
-// tokens' way from L1 would (16 tokens: 512 bytes of tokens for 32 of weights).
+// tokens' way from L1 would (16 tokens: 512 bytes of tokens for 32 of weights).  Measured,
+// 2,304 x 2,304 fp32 (3.2 us at the copy rate): 1 token 12 us, 5 tokens 13, 16 tokens 25, where the
+// tensor cores' three launches take 33.
 #include <algorithm>
 
 #include "common.cuh"

@@ -9,6 +9,11 @@
 // CTA for itself where they are small, else by a launch before this one, in both cases
 // while the first weights are already on their way; beyond that every weight is widened
 // once for all tokens.  The tokens' columns come from L1 and L2.
+//
+// Measured, 8 tokens, bf16, 9,216 columns, 2,304 outputs: 14.4 us cold for 42 MB, 45% of the copy rate
+// (6.5 us): the launch, the first loads' latency and the last sums are as long as the stream.
+// One token, int8, 2,304 columns, 9,216 gated outputs: 17 us with its digits made in place, again
+// 42 MB.
 #include <algorithm>
 
 #include "common.cuh"

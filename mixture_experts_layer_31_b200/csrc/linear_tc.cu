@@ -31,7 +31,13 @@
 // weight, as the routed layer's tensor-core path has it: measured against 64 bits 2.2 x 10^-3
 // where y's own rounding alone leaves 1.7 x 10^-3), in three parts where y is fp32.
 // The pass costs 3 bytes or 2.6 per weight, most of it in L2, against 2 M operations per
-// weight: a few percent from a thousand tokens on.
+// weight.
+//
+// Measured: 4,096 tokens, 2,304 columns, 9,216 gated outputs, bf16, 219 us alone (1,586 TFLOP/s, 97%
+// of the rate of a large library product, the tensor pipe 81% busy) and 250 to 290 us in a
+// loop, where the power limit lowers the clock; 1,999 tokens, 9,216 columns, 2,304 outputs,
+// int8, 66 us after a widening pass of 20; 2,048 tokens, 2,304 x 2,304, fp32, 120 us.  L2 is at
+// half its rate meanwhile.
 #include <cuda.h>
 
 #include <algorithm>

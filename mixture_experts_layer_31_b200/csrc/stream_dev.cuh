@@ -21,7 +21,8 @@
 // token, each digit a column of its own of an integer matrix instruction: sums are exact,
 // and only the rounding of x to 2^(e - 31) (the 31st bit below the token's largest value; a
 // bf16 value keeps all its bits down to 2^-22 of that) stands for the 8 bits of each bf16
-// product.  Measured on 16 tokens: 256 us with widened codes, see the layer's kernel.
+// product.  Measured in the few-token layer: 4 tokens int8 117 us with widened codes and 108
+// with digits, 16 tokens 255 and 240.
 #pragma once
 #include <type_traits>
 
