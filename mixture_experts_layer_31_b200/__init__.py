@@ -321,6 +321,10 @@ def _raw_stream(torch, device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+def _capturing(torch) -> bool:
+    return torch._C._cuda_isCurrentStreamCapturing()
+
+
 class MoELayer:
     """Device-resident layer: holds the weights as torch CUDA tensors, a reusable
     workspace, and calls moe_route / moe_forward on the current torch stream."""
@@ -447,12 +451,15 @@ class MoELayer:
         return y
 
     def few_workspace(self, T: int, stream: int = 0):
-        """The workspace of few() calls on one stream (they run in order and share it)."""
+        """The workspace of few() calls on one stream (they run in order and share it).  A call
+        that is being captured gets one of its own, which lives in its graph's memory."""
         ws = self._few_ws.get(stream)
-        if ws is None or ws[0] < T:
+        capturing = _capturing(self.torch)
+        if capturing or ws is None or ws[0] < T:
             n = moe_few_workspace_size(self.desc, self.shared, T)
-            ws = self._few_ws[stream] = (T, self.torch.empty(max(n, 256), dtype=self.torch.uint8,
-                                                             device=self.tensors["W_r"].device))
+            ws = (T, self.torch.empty(max(n, 256), dtype=self.torch.uint8, device=self.tensors["W_r"].device))
+            if not capturing:
+                self._few_ws[stream] = ws
         return ws[1]
 
     def few(self, x, residual=None, out=None):
@@ -460,8 +467,7 @@ class MoELayer:
         route, routed experts, the shared expert (if the layer has one) and residual (if
         given, [T, H] in x's dtype).  x [T, H] contiguous; returns (y, idx, w), written into
         `out` = (y, idx, w) if given (y may be residual itself).  Calls on one stream share a
-        workspace that the layer keeps; so do the graphs captured on one stream: replay
-        those in order, or capture them from layers of their own."""
+        workspace that the layer keeps; a captured call has one in its graph's memory."""
         torch, d, device = self.torch, self.desc, self.tensors["W_r"].device
         H, k, dtype = d.H, d.k, self.x_dtype
         T = x.shape[0]
@@ -530,21 +536,23 @@ class Linear:
         self._need = {}  # workspace bytes by M
 
     def workspace(self, M: int, stream: int = 0):
-        """The workspace of the calls on one stream (they run in order and share it)."""
+        """The workspace of the calls on one stream (they run in order and share it).  A call that
+        is being captured gets one of its own, which lives in its graph's memory."""
         n = self._need.get(M)
         if n is None:
             n = self._need[M] = moe_linear_workspace_size(self.desc, M)
         ws = self._ws.get(stream)
-        if ws is None or ws.numel() < n:
-            ws = self._ws[stream] = self.torch.empty(max(n, 256), dtype=self.torch.uint8,
-                                                     device=self.tensors["W"].device)
+        capturing = _capturing(self.torch)
+        if capturing or ws is None or ws.numel() < n:
+            ws = self.torch.empty(max(n, 256), dtype=self.torch.uint8, device=self.tensors["W"].device)
+            if not capturing:
+                self._ws[stream] = ws
         return ws
 
     def __call__(self, x, residual=None, y=None):
         """x [M, K], rows contiguous but any (16-byte) distance apart; residual and y [M, N]
         with contiguous rows; y may be residual itself.  Calls on one stream share a workspace
-        that the object keeps; so do the graphs captured on one stream: replay those in
-        order, or capture them from objects of their own."""
+        that the object keeps; a captured call has one in its graph's memory."""
         torch, d, device = self.torch, self.desc, self.tensors["W"].device
         K, N, dtype = d.K, d.N, self.y_dtype
         M = x.shape[0]

@@ -317,6 +317,30 @@ def test_captured_and_replayed_with_new_inputs():
         layer.judge(new, *out)
 
 
+@pytest.mark.parametrize("wfmt,xfmt", [("int8", "bf16"), ("f32", "f32")])
+def test_graphs_keep_workspaces_of_their_own(wfmt, xfmt):
+    """Two captured calls replayed at once, after the eager workspace was replaced by a larger one."""
+    layer = Layer(E=64, k=8, H=512, I=512, wfmt=wfmt, xfmt=xfmt)
+    xs = [layer.x(3, 60 + n).cuda() for n in range(2)]
+    want = [[t.clone() for t in layer.dev.few(x)] for x in xs]
+    outs, graphs = [tuple(torch.zeros_like(t) for t in w) for w in want], []
+    for x, out in zip(xs, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            layer.dev.few(x, out=out)
+    layer.dev.few(layer.x(16).cuda())
+    other = [torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda") for _ in range(16)]
+    streams = [torch.cuda.Stream() for _ in graphs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for out, w in zip(outs, want) for a, b in zip(out, w))
+    assert all(bool((t == 255).all()) for t in other)
+
+
 def test_two_streams_at_once():
     """Calls that overlap on the GPU, each stream with its own workspace: many at once."""
     layer = Layer(E=64, k=8, H=512, I=512, wfmt="bf16")

@@ -208,6 +208,30 @@ def test_captured_and_replayed_with_new_inputs(M):
         p.judge(new, y)
 
 
+@pytest.mark.parametrize("wfmt,xfmt,M", [("int8", "bf16", 4), ("int4", "bf16", 60), ("f32", "f32", 100)])
+def test_graphs_keep_workspaces_of_their_own(wfmt, xfmt, M):
+    """Two captured calls replayed at once, after the eager workspace was replaced by a larger one."""
+    p = Product(1024, 320, wfmt, xfmt)
+    xs = [p.x(M, 60 + n).cuda() for n in range(2)]
+    want = [p.dev(x).clone() for x in xs]
+    ys, graphs = [torch.empty_like(w) for w in want], []
+    for x, y in zip(xs, ys):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            p.dev(x, y=y)
+    p.dev(p.x(M + 200).cuda())
+    other = [torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda") for _ in range(16)]
+    streams = [torch.cuda.Stream() for _ in graphs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, w) for y, w in zip(ys, want))
+    assert all(bool((t == 255).all()) for t in other)
+
+
 @pytest.mark.parametrize("M", [2, 48, 160])
 def test_several_streams_at_once(M):
     p = Product(2048, 320, "int8")
