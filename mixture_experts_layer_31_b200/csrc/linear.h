@@ -70,14 +70,14 @@ cudaError_t launch_linear_stream(const moe_linear_desc& d, const LinearArgs& a, 
 // fp32 tokens or weights: up to this many tokens a warp computes rows of W in fp32
 constexpr int kLinearRowTokens = 16;
 cudaError_t launch_linear_rows(const moe_linear_desc& d, const LinearArgs& a, int num_sms, cudaStream_t s);
-// beyond that, tensor cores: quantised and fp32 weights are first widened into bf16 (parts) in the
-// workspace, one launch per matrix, fp32 tokens likewise; where linear_tc_split() a last launch
-// adds up the parts of the reduction
+// beyond that, tensor cores: quantised and fp32 weights and fp32 tokens are first widened into bf16
+// (parts) in the workspace, by one launch; where linear_tc_split() a last launch adds up the
+// parts of the reduction
 bool linear_tc_ok(const moe_linear_desc& d, int M);
 size_t linear_tc_workspace(const moe_linear_desc& d, int M);
 bool linear_tc_split(const moe_linear_desc& d, int M);
-cudaError_t launch_linear_widen(const moe_linear_desc& d, int M, int which, void* workspace, int num_sms, cudaStream_t s);
-cudaError_t launch_linear_split_x(const moe_linear_desc& d, const LinearArgs& a, void* workspace, int num_sms, cudaStream_t s);
+bool linear_tc_layouts(const moe_linear_desc& d);  // a launch that lays operands out comes first
+cudaError_t launch_linear_layouts(const moe_linear_desc& d, const LinearArgs& a, void* workspace, int num_sms, cudaStream_t s);
 cudaError_t launch_linear_tc(const moe_linear_desc& d, const LinearArgs& a, void* workspace, int num_sms, uint32_t* flags,
                              cudaStream_t s);
 cudaError_t launch_linear_sum(const moe_linear_desc& d, const LinearArgs& a, void* workspace, int num_sms, cudaStream_t s);

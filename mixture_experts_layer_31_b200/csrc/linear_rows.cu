@@ -3,7 +3,7 @@
 // weights' way from HBM bounds it; R rows share a token's columns, without which the
 // tokens' way from L1 would (16 tokens: 512 bytes of tokens for 32 of weights).  Measured,
 // 2,304 x 2,304 fp32 (3.2 us at the copy rate): 1 token 12 us, 5 tokens 13, 16 tokens 25, where the
-// tensor cores' three launches take 33.
+// tensor cores' three launches take 31.
 #include <algorithm>
 
 #include "common.cuh"

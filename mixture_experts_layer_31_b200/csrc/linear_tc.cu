@@ -36,7 +36,7 @@
 // Measured: 4,096 tokens, 2,304 columns, 9,216 gated outputs, bf16, 219 us alone (1,586 TFLOP/s, 97%
 // of the rate of a large library product, the tensor pipe 81% busy) and 250 to 290 us in a
 // loop, where the power limit lowers the clock; 1,999 tokens, 9,216 columns, 2,304 outputs,
-// int8, 66 us after a widening pass of 20; 2,048 tokens, 2,304 x 2,304, fp32, 120 us.  L2 is at
+// int8, 66 us after a widening pass of 13; 2,048 tokens, 2,304 x 2,304, fp32, 117 us.  L2 is at
 // half its rate meanwhile.
 #include <cuda.h>
 
@@ -507,7 +507,7 @@ __device__ __forceinline__ void split3(float x, uint16_t (&p)[3]) {
 }
 
 // The passes below take kItems pieces of 8 values per thread and step, their loads first: with one
-// piece at a time the loads' latency was most of the time (9,216 x 2,304 int8: 20 us, now WIDEN_NEW).
+// piece at a time the loads' latency was most of the time (9,216 x 2,304 int8: 20 us, so 13).
 constexpr int kItems = 4;
 
 // The code of column j of 8 int4 codes, times s: the code plus 2^23 + 8 is made by its bits, which
@@ -520,10 +520,8 @@ __device__ __forceinline__ float int4_value(uint32_t codes, int j, float s) {
 // Each row to its three parts, [3][rows][pitch], zero between cols and pitch.  WF: fp32, or int4
 // codes times their block scales in fp32.
 template <int WF>
-__global__ void __launch_bounds__(256) linear_split_kernel(const void* __restrict__ W, const float* __restrict__ s, long long ld,
-                                                           int rows, int cols, int pitch, uint16_t* __restrict__ out) {
-  pdl_wait();
-  pdl_trigger();
+__device__ __forceinline__ void split_rows(const void* __restrict__ W, const float* __restrict__ s, long long ld, int rows,
+                                           int cols, int pitch, uint16_t* __restrict__ out) {
   const int eights = pitch / 8;
   const size_t n = (size_t)rows * eights, plane = (size_t)rows * pitch;
   constexpr int kAtOnce = kItems / 2;
@@ -570,10 +568,8 @@ __global__ void __launch_bounds__(256) linear_split_kernel(const void* __restric
 
 // stored weights to bf16
 template <int WF>
-__global__ void __launch_bounds__(256) linear_widen_kernel(const void* __restrict__ W, const float* __restrict__ s, size_t n8,
-                                                           uint16_t* __restrict__ out) {
-  pdl_wait();
-  pdl_trigger();
+__device__ __forceinline__ void widen_values(const void* __restrict__ W, const float* __restrict__ s, size_t n8,
+                                             uint16_t* __restrict__ out) {
   for (size_t i0 = (size_t)blockIdx.x * 256 * kItems + threadIdx.x; i0 < n8; i0 += (size_t)gridDim.x * 256 * kItems) {
     uint2 q[kItems] = {};
     float scale[kItems] = {};
@@ -608,6 +604,25 @@ __global__ void __launch_bounds__(256) linear_widen_kernel(const void* __restric
       *reinterpret_cast<uint4*>(out + 8 * i) = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
+}
+
+// Everything a call has to lay out anew, by blockIdx.y, in one launch: W, W_up and fp32 tokens.
+struct Layouts {
+  const void* from[3];
+  const float* s[3];
+  uint16_t* to[3];
+  int x, rows_w, rows_x, K, pitch;  // which one holds the tokens, -1 for none
+  long long ldx;
+};
+
+template <int WF, bool SPLIT>
+__global__ void __launch_bounds__(256) linear_layout_kernel(const __grid_constant__ Layouts p) {
+  pdl_wait();
+  pdl_trigger();
+  const int j = blockIdx.y;
+  if (j == p.x) split_rows<MOE_W_F32>(p.from[j], nullptr, p.ldx, p.rows_x, p.K, p.pitch, p.to[j]);
+  else if constexpr (SPLIT) split_rows<WF>(p.from[j], p.s[j], p.K, p.rows_w, p.K, p.pitch, p.to[j]);
+  else if constexpr (WF != MOE_W_F32) widen_values<WF>(p.from[j], p.s[j], (size_t)p.rows_w * p.K / 8, p.to[j]);
 }
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -673,35 +688,37 @@ static dim3 grid_for(size_t items, int num_sms) {
   return dim3((unsigned)std::min<size_t>((items + 255) / 256, (size_t)num_sms * 8));
 }
 
-cudaError_t launch_linear_widen(const moe_linear_desc& d, int M, int which, void* workspace, int num_sms, cudaStream_t s) {
-  const TcLayout t = tc_layout(d, M);
-  const void* W = which ? d.W_up : d.W;
-  const float* sc = which ? d.s_up : d.s;
-  uint16_t* out = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + t.w[which]);
-  const dim3 block(256);
-  if (t.wparts == 3) {
-    const dim3 grid = grid_for((size_t)d.N * t.pitch / (4 * kItems), num_sms);
-    auto go = [&](auto kernel) {
-      return launch_next(which == 0, kernel, grid, block, 0, s, W, sc, (long long)d.K, d.N, d.K, t.pitch, out);
-    };
-    return d.wfmt == MOE_W_F32 ? go(linear_split_kernel<MOE_W_F32>)
-                               : (d.wfmt == MOE_W_INT4_B32 ? go(linear_split_kernel<MOE_W_INT4_B32>)
-                                                           : go(linear_split_kernel<MOE_W_INT4_B128>));
-  }
-  const size_t n8 = (size_t)d.N * d.K / 8;
-  const dim3 grid = grid_for(n8 / kItems, num_sms);
-  switch (d.wfmt) {
-    case MOE_W_INT8_ROW: return launch_next(which == 0, linear_widen_kernel<MOE_W_INT8_ROW>, grid, block, 0, s, W, sc, n8, out);
-    case MOE_W_INT4_B32: return launch_next(which == 0, linear_widen_kernel<MOE_W_INT4_B32>, grid, block, 0, s, W, sc, n8, out);
-    default: return launch_next(which == 0, linear_widen_kernel<MOE_W_INT4_B128>, grid, block, 0, s, W, sc, n8, out);
-  }
-}
+bool linear_tc_layouts(const moe_linear_desc& d) { return d.wfmt != MOE_W_BF16 || d.xfmt == MOE_X_F32; }
 
-cudaError_t launch_linear_split_x(const moe_linear_desc& d, const LinearArgs& a, void* workspace, int num_sms, cudaStream_t s) {
+cudaError_t launch_linear_layouts(const moe_linear_desc& d, const LinearArgs& a, void* workspace, int num_sms, cudaStream_t s) {
   const TcLayout t = tc_layout(d, a.M);
-  return launch_next(!t.w_copy, linear_split_kernel<MOE_W_F32>, grid_for((size_t)a.M * t.pitch / (4 * kItems), num_sms), dim3(256), 0, s, a.x,
-                     static_cast<const float*>(nullptr), a.ldx, a.M, d.K, t.pitch,
-                  reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + t.x));
+  char* ws = static_cast<char*>(workspace);
+  Layouts p = {};
+  p.x = -1, p.rows_w = d.N, p.rows_x = a.M, p.K = d.K, p.pitch = t.pitch, p.ldx = a.ldx;
+  int n = 0;
+  size_t most = 0;
+  auto add = [&](const void* from, const float* sc, size_t to, size_t rows) {
+    p.from[n] = from, p.s[n] = sc, p.to[n] = reinterpret_cast<uint16_t*>(ws + to);
+    most = std::max(most, rows * t.pitch);
+    ++n;
+  };
+  for (int i = 0; t.w_copy && i < (d.W_up ? 2 : 1); ++i) add(a.W[i], a.s[i], t.w[i], (size_t)d.N);
+  if (t.xparts == 3) {
+    p.x = n;
+    add(a.x, nullptr, t.x, (size_t)a.M);
+  }
+  const size_t blocks = (most / 8 + 256 * kItems - 1) / (256 * kItems);
+  const dim3 grid((unsigned)std::min<size_t>(blocks, (size_t)num_sms * 8), n);
+  auto go = [&](auto kernel) { return launch_k(kernel, grid, dim3(256), 0, s, p); };
+  const bool split = t.wparts == 3;
+  switch (d.wfmt) {
+    case MOE_W_INT8_ROW: return go(linear_layout_kernel<MOE_W_INT8_ROW, false>);
+    case MOE_W_INT4_B32:
+      return split ? go(linear_layout_kernel<MOE_W_INT4_B32, true>) : go(linear_layout_kernel<MOE_W_INT4_B32, false>);
+    case MOE_W_INT4_B128:
+      return split ? go(linear_layout_kernel<MOE_W_INT4_B128, true>) : go(linear_layout_kernel<MOE_W_INT4_B128, false>);
+    default: return go(linear_layout_kernel<MOE_W_F32, true>);  // fp32 weights, or fp32 tokens alone
+  }
 }
 
 static TcArgs tc_args(const moe_linear_desc& d, const LinearArgs& a, const TcLayout& t, void* workspace) {
@@ -741,7 +758,7 @@ cudaError_t launch_linear_tc(const moe_linear_desc& d, const LinearArgs& a, void
   if (e != cudaSuccess) return e;
   const long long tiles = (long long)t.mt * t.nt * t.splits;
   const int pairs = (int)std::min<long long>(tiles, num_sms / 2);
-  return launch_next(!t.w_copy && t.xparts == 1, kernel, dim3(2 * pairs), dim3(kThreads), kSmem, s, mx, mw[0], mw[1], p, flags);
+  return launch_next(!linear_tc_layouts(d), kernel, dim3(2 * pairs), dim3(kThreads), kSmem, s, mx, mw[0], mw[1], p, flags);
 }
 
 bool linear_tc_split(const moe_linear_desc& d, int M) { return tc_layout(d, M).splits > 1; }

@@ -715,11 +715,8 @@ extern "C" moe_status moe_linear(const moe_linear_desc* d, const void* x, int64_
     return MOE_OK;
   }
   if (linear_tc_ok(*d, M)) {
-    if (d->wfmt != MOE_W_BF16)
-      for (int i = 0; i < (d->W_up ? 2 : 1); ++i)
-        MOE_LAUNCH("linear_widen", stream, launch_linear_widen(*d, M, i, workspace, dev->num_sms, stream));
-    if (d->xfmt == MOE_X_F32)
-      MOE_LAUNCH("linear_split_x", stream, launch_linear_split_x(*d, a, workspace, dev->num_sms, stream));
+    if (linear_tc_layouts(*d))
+      MOE_LAUNCH("linear_layouts", stream, launch_linear_layouts(*d, a, workspace, dev->num_sms, stream));
     MOE_LAUNCH("linear_tc", stream, launch_linear_tc(*d, a, workspace, dev->num_sms, dev->flags, stream));
     if (linear_tc_split(*d, M))
       MOE_LAUNCH("linear_sum", stream, launch_linear_sum(*d, a, workspace, dev->num_sms, stream));
