@@ -51,7 +51,7 @@ class Layer:
     def x(self, T, seed=7):
         return torch.from_numpy(synth.normal_f32((T, self.H), seed, 9, 0.0, 1.0)).to(self.x_dtype)
 
-    def judge(self, x, y, idx, w, residual=None, what=""):
+    def compare(self, x, y, idx, w, residual=None, what=""):
         ri, rw = ref.route(x, self.W_r, self.b, self.mask, self.k, self.router, self.scale)
         assert torch.equal(idx.cpu(), ri), what
         # weights: one division and one product in 64 bits, one rounding to fp32
@@ -64,7 +64,7 @@ class Layer:
         r = self.x(T, seed + 1000) if residual else None
         y, idx, w = self.dev.few(x.cuda(), residual=None if r is None else r.cuda())
         torch.cuda.synchronize()
-        self.judge(x, y, idx, w, r, "T=%d" % T)
+        self.compare(x, y, idx, w, r, "T=%d" % T)
         return x, y, idx, w
 
 
@@ -155,7 +155,7 @@ def test_fewer_selectable_experts_than_slots(active):
     x = layer.x(3)
     y, idx, w = layer.dev.few(x.cuda(), residual=x.cuda())
     assert moe.moe_device_flags(clear=True) == 2  # MOE_FLAG_TOO_FEW_ACTIVE
-    layer.judge(x, y, idx, w, x)
+    layer.compare(x, y, idx, w, x)
     assert bool((idx[:, len(active):] == -1).all()) and bool((w[:, len(active):] == 0).all())
 
 
@@ -195,7 +195,7 @@ def test_tokens_of_any_magnitude(wfmt, scale):
     layer = Layer(wfmt=wfmt, bias=False)
     x = (layer.x(3).float() * torch.tensor([1.0, scale, 0.0])[:, None]).to(torch.bfloat16)
     y, idx, w = layer.dev.few(x.cuda())
-    layer.judge(x, y, idx, w)
+    layer.compare(x, y, idx, w)
 
 
 @pytest.mark.parametrize("wfmt", ["bf16", "int8", "int4"])
@@ -207,7 +207,7 @@ def test_outliers_in_a_token(wfmt):
     x[1, 200] = -30000.0
     x = x.to(torch.bfloat16)
     y, idx, w = layer.dev.few(x.cuda())
-    layer.judge(x, y, idx, w)
+    layer.compare(x, y, idx, w)
 
 
 def test_beside_other_work():
@@ -236,7 +236,7 @@ def test_large_activations_overflow_no_sooner_than_fp32():
     layer = Layer()
     x = layer.x(2) * 300
     y, idx, w = layer.dev.few(x.to(torch.bfloat16).cuda())
-    layer.judge(x.to(torch.bfloat16), y, idx, w)
+    layer.compare(x.to(torch.bfloat16), y, idx, w)
 
 
 def test_ties_go_to_the_lower_expert():
@@ -314,7 +314,7 @@ def test_captured_and_replayed_with_new_inputs():
         g.replay()
         g.replay()
         torch.cuda.synchronize()
-        layer.judge(new, *out)
+        layer.compare(new, *out)
 
 
 @pytest.mark.parametrize("wfmt,xfmt", [("int8", "bf16"), ("f32", "f32")])
@@ -398,9 +398,9 @@ def test_dense_layer_then_routed_layers():
         x.copy_(new)
         g.replay()
         torch.cuda.synchronize()
-        # each step is judged on the inputs that it had
+        # each step is compared on the inputs that it had
         want, bound = ref.linear(new, dg, None, (du, None), "silu", None, torch.bfloat16, "int8")
         ref.check(h, want, bound, "up")
         want, bound = ref.linear(h.cpu(), dd, None, None, "none", new, torch.bfloat16, "int8")
         ref.check(y, want, bound, "down")
-        layer.judge(y.cpu(), z, idx, w, y.cpu(), "routed")
+        layer.compare(y.cpu(), z, idx, w, y.cpu(), "routed")

@@ -39,7 +39,7 @@ class Product:
     def residual(self, M, seed=8):
         return torch.from_numpy(synth.normal_f32((M, self.N), seed, 9, 0.0, 1.0)).to(self.y_dtype)
 
-    def judge(self, x, y, residual=None, what=""):
+    def compare(self, x, y, residual=None, what=""):
         # int4 weights are widened exactly for up to 40 tokens and for fp32 outputs; else each is rounded
         # to bf16 once, which is off by half a step of bf16 at most (moe_linear)
         exact = x.shape[0] <= 40 or self.y_dtype == torch.float32
@@ -52,7 +52,7 @@ class Product:
         r = self.residual(M) if residual else None
         y = self.dev(x.cuda(), residual=None if r is None else r.cuda())
         torch.cuda.synchronize()
-        self.judge(x, y, r, "M=%d" % M)
+        self.compare(x, y, r, "M=%d" % M)
         return x, y
 
 
@@ -130,7 +130,7 @@ def test_strided_rows_and_untouched_neighbours(wfmt, xfmt, M):
     xs[:M, : p.K], rs[:M, : p.N] = x.cuda(), r.cuda()
     p.dev(xs[:M, : p.K], residual=rs[:M, : p.N], y=ys[:M, : p.N])
     torch.cuda.synchronize()
-    p.judge(x, ys[:M, : p.N], r)
+    p.compare(x, ys[:M, : p.N], r)
     assert bool((ys[M:] == 5).all()) and bool((ys[:, p.N:] == 5).all())
 
 
@@ -162,7 +162,7 @@ def test_tokens_of_any_magnitude(wfmt, scale):
     """Digits are relative to the token's largest value: its magnitude does not matter."""
     p = Product(512, 80, wfmt, yfmt="f32")
     x = (p.x(2).float() * torch.tensor([scale, 0.0])[:, None]).to(torch.bfloat16)
-    p.judge(x, p.dev(x.cuda()))
+    p.compare(x, p.dev(x.cuda()))
 
 
 @pytest.mark.parametrize("wfmt,xfmt", [("bf16", "bf16"), ("int8", "bf16"), ("int4", "bf16"), ("f32", "f32")])
@@ -174,7 +174,7 @@ def test_outliers_in_a_row(wfmt, xfmt, M):
     x[:, 7] *= 4000
     x[0, 200] = -30000.0
     x = x.to(p.x_dtype)
-    p.judge(x, p.dev(x.cuda()))
+    p.compare(x, p.dev(x.cuda()))
 
 
 @pytest.mark.parametrize("wfmt,xfmt", [("bf16", "bf16"), ("int8", "bf16"), ("int4", "bf16"), ("f32", "f32")])
@@ -205,7 +205,7 @@ def test_captured_and_replayed_with_new_inputs(M):
         g.replay()
         g.replay()
         torch.cuda.synchronize()
-        p.judge(new, y)
+        p.compare(new, y)
 
 
 @pytest.mark.parametrize("wfmt,xfmt,M", [("int8", "bf16", 4), ("int4", "bf16", 60), ("f32", "f32", 100)])
@@ -280,7 +280,7 @@ def test_row_offsets_beyond_32_bits(N):
         y = base[:, 4096 : 4096 + N]
         p.dev(base[:, :K], y=y)
         torch.cuda.synchronize()
-        p.judge(x, y)
+        p.compare(x, y)
         del base, y
 
 
