@@ -44,8 +44,8 @@ __device__ __forceinline__ void load4(const void* base, size_t i, float (&v)[4])
   }
 }
 
-// One CTA per kRouterExperts experts.  Its warps share out the columns; each keeps the sums of
-// all tokens (in passes of TT) so that a router weight is widened to 64 bits once for all of
+// One CTA per kRouterExperts experts and TT tokens.  Its warps share out the columns; each keeps
+// the sums of all its tokens so that a router weight is widened to 64 bits once for all of
 // them: the conversions, not the 64-bit multiply-adds, are what this costs (a token for each
 // warp instead took 20 us at 16 tokens x 2,304 columns x 256 experts).
 constexpr int kRouterExperts = 2;
@@ -60,12 +60,13 @@ __global__ void __launch_bounds__(kRouterThreads)
   pdl_trigger();
   constexpr int kSums = kRouterExperts * TT, kRWarps = kRouterThreads / 32;
   __shared__ double part[kRWarps][kSums];
-  const int e0 = blockIdx.x * kRouterExperts, tid = threadIdx.x, w = warp_id(), lane = lane_id();
-  if (blockIdx.x == 0)
+  const int e0 = blockIdx.x * kRouterExperts, t0 = blockIdx.y * TT, tid = threadIdx.x, w = warp_id(), lane = lane_id();
+  if (blockIdx.x == 0 && blockIdx.y == 0)
     for (int i = tid; i < kFewCounters; i += kRouterThreads) counters[i] = 0;
   if (e0 >= E) {
     // the CTAs past the experts: a token each, as digits for the integer products
-    const int t = blockIdx.x - (E + kRouterExperts - 1) / kRouterExperts;
+    const int t = t0 + blockIdx.x - (E + kRouterExperts - 1) / kRouterExperts;
+    if (t >= T) return;
     __shared__ float warps[kRouterThreads / 32];
     if constexpr (XF == MOE_X_BF16)
       stream::write_digits(static_cast<const uint16_t*>(x) + (size_t)t * H, H, int4, digits + (size_t)t * 4 * stream::digit_pitch(H),
@@ -75,65 +76,62 @@ __global__ void __launch_bounds__(kRouterThreads)
   const float* row[kRouterExperts];
 #pragma unroll
   for (int i = 0; i < kRouterExperts; ++i) row[i] = W_r + (size_t)min(e0 + i, E - 1) * H;
-  for (int t0 = 0; t0 < T; t0 += TT) {
-    double acc[kSums] = {};
+  double acc[kSums] = {};
 #pragma unroll 2
-    for (int c = w * 128 + lane * 4; c < H; c += kRWarps * 128) {
-      float v[kRouterExperts][4], u[TT][4];
+  for (int c = w * 128 + lane * 4; c < H; c += kRWarps * 128) {
+    float v[kRouterExperts][4], u[TT][4];
 #pragma unroll
-      for (int i = 0; i < kRouterExperts; ++i) load4<MOE_X_F32>(row[i], c, v[i]);
+    for (int i = 0; i < kRouterExperts; ++i) load4<MOE_X_F32>(row[i], c, v[i]);
 #pragma unroll
-      for (int j = 0; j < TT; ++j) load4<XF>(x, (size_t)min(t0 + j, T - 1) * H + c, u[j]);
+    for (int j = 0; j < TT; ++j) load4<XF>(x, (size_t)min(t0 + j, T - 1) * H + c, u[j]);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        double wd[kRouterExperts];
+    for (int q = 0; q < 4; ++q) {
+      double wd[kRouterExperts];
 #pragma unroll
-        for (int i = 0; i < kRouterExperts; ++i) wd[i] = (double)v[i][q];
+      for (int i = 0; i < kRouterExperts; ++i) wd[i] = (double)v[i][q];
 #pragma unroll
-        for (int j = 0; j < TT; ++j) {
-          const double xd = (double)u[j][q];
+      for (int j = 0; j < TT; ++j) {
+        const double xd = (double)u[j][q];
 #pragma unroll
-          for (int i = 0; i < kRouterExperts; ++i) acc[j * kRouterExperts + i] = fma(wd[i], xd, acc[j * kRouterExperts + i]);
-        }
+        for (int i = 0; i < kRouterExperts; ++i) acc[j * kRouterExperts + i] = fma(wd[i], xd, acc[j * kRouterExperts + i]);
       }
     }
-    // sums over the lanes: halves of the values change sides until each lane has at most one
-    int n = kSums, first = 0;
+  }
+  // sums over the lanes: halves of the values change sides until each lane has at most one
+  int n = kSums, first = 0;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      if (n > 1) {
-        n >>= 1;
-        const bool up = (lane & off) != 0;
+  for (int off = 16; off > 0; off >>= 1) {
+    if (n > 1) {
+      n >>= 1;
+      const bool up = (lane & off) != 0;
 #pragma unroll
-        for (int k = 0; k < kSums / 2; ++k) {
-          if (k >= n) break;
-          const double give = up ? acc[k] : acc[k + n], keep = up ? acc[k + n] : acc[k];
-          acc[k] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, off);
-        }
-        if (up) first += n;
-      } else {
-        acc[0] += __shfl_xor_sync(0xFFFFFFFFu, acc[0], off);
+      for (int k = 0; k < kSums / 2; ++k) {
+        if (k >= n) break;
+        const double give = up ? acc[k] : acc[k + n], keep = up ? acc[k + n] : acc[k];
+        acc[k] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, off);
       }
+      if (up) first += n;
+    } else {
+      acc[0] += __shfl_xor_sync(0xFFFFFFFFu, acc[0], off);
     }
-    part[w][first] = acc[0];  // lanes with the same value write the same sum
-    __syncthreads();
-    const int j = tid / kRouterExperts, e = e0 + tid % kRouterExperts, t = t0 + j;
-    if (tid < kSums && t < T && e < E) {
-      double l = 0.0;
+  }
+  part[w][first] = acc[0];  // lanes with the same value write the same sum
+  __syncthreads();
+  const int j = tid / kRouterExperts, e = e0 + tid % kRouterExperts, t = t0 + j;
+  if (tid < kSums && t < T && e < E) {
+    double l = 0.0;
 #pragma unroll
-      for (int i = 0; i < kRWarps; ++i) l += part[i][tid];
-      const bool finite = isfinite((float)l);
-      if (!finite) raise_flag(flags, MOE_FLAG_NONFINITE_LOGIT);
-      double score = l, key = l;
-      if (router == MOE_ROUTER_SIGMOID_BIAS) {
-        score = 1.0 / (1.0 + exp(-l));
-        key = score + (bias ? (double)bias[e] : 0.0);
-      }
-      const bool open = finite && key == key && (mask == nullptr || mask[e] != 0);
-      keys[(size_t)t * E + e] = open ? sortable(key) : 0;
-      scores[(size_t)t * E + e] = score;
+    for (int i = 0; i < kRWarps; ++i) l += part[i][tid];
+    const bool finite = isfinite((float)l);
+    if (!finite) raise_flag(flags, MOE_FLAG_NONFINITE_LOGIT);
+    double score = l, key = l;
+    if (router == MOE_ROUTER_SIGMOID_BIAS) {
+      score = 1.0 / (1.0 + exp(-l));
+      key = score + (bias ? (double)bias[e] : 0.0);
     }
-    __syncthreads();
+    const bool open = finite && key == key && (mask == nullptr || mask[e] != 0);
+    keys[(size_t)t * E + e] = open ? sortable(key) : 0;
+    scores[(size_t)t * E + e] = score;
   }
 }
 
@@ -1168,16 +1166,18 @@ cudaError_t launch_few_router(const moe_desc& d, const moe_shared_expert* sh, co
                               uint32_t* flags, cudaStream_t s) {
   const FewLayout l = few_layout(d, sh ? sh->I : 0, T);
   char* ws = static_cast<char*>(workspace);
-  auto go = [&](auto kernel) {
-    const int ctas = (d.E + kRouterExperts - 1) / kRouterExperts + (few_digits(d) ? T : 0);
-    return launch_k(kernel, dim3(ctas), dim3(kRouterThreads), 0, s, x, d.W_r, d.b, d.expert_mask, T, d.H, d.E, d.router,
+  auto go = [&](auto kernel, int tokens) {
+    const dim3 grid((d.E + kRouterExperts - 1) / kRouterExperts + (few_digits(d) ? std::min(T, tokens) : 0), (T + tokens - 1) / tokens);
+    return launch_k(kernel, grid, dim3(kRouterThreads), 0, s, x, d.W_r, d.b, d.expert_mask, T, d.H, d.E, d.router,
                     reinterpret_cast<uint64_t*>(ws + l.keys), reinterpret_cast<double*>(ws + l.scores),
                     reinterpret_cast<uint32_t*>(ws), reinterpret_cast<int8_t*>(ws + l.digits),
                     (int)(d.wfmt != MOE_W_INT8_ROW), reinterpret_cast<float*>(ws + l.units), flags);
   };
   if (d.xfmt == MOE_X_F32)
-    return T == 1 ? go(few_router_kernel<MOE_X_F32, 1>) : (T <= 4 ? go(few_router_kernel<MOE_X_F32, 4>) : go(few_router_kernel<MOE_X_F32, 8>));
-  return T == 1 ? go(few_router_kernel<MOE_X_BF16, 1>) : (T <= 4 ? go(few_router_kernel<MOE_X_BF16, 4>) : go(few_router_kernel<MOE_X_BF16, 8>));
+    return T == 1 ? go(few_router_kernel<MOE_X_F32, 1>, 1)
+                  : (T <= 4 ? go(few_router_kernel<MOE_X_F32, 4>, 4) : go(few_router_kernel<MOE_X_F32, 8>, 8));
+  return T == 1 ? go(few_router_kernel<MOE_X_BF16, 1>, 1)
+                : (T <= 4 ? go(few_router_kernel<MOE_X_BF16, 4>, 4) : go(few_router_kernel<MOE_X_BF16, 8>, 8));
 }
 
 cudaError_t launch_few_layer(const moe_desc& d, const moe_shared_expert* sh, const void* x, int T, int32_t* idx,
