@@ -710,11 +710,13 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     for (int i = have; i < R::kStages; ++i) issue_next();
   };
   if (!sh.taken) fill(issued);
-  // this warp's tokens' experts, for the weights later; then the plan's space becomes the units' sums
+  // this warp's tokens' experts, for the weights later (warp 0 will wait for the grid meanwhile, so
+  // it comes last); then the plan's space becomes the units' sums
+  const int my_t = kWarps - 1 - w;
   int my_e[2] = {-1, -1};
 #pragma unroll
   for (int i = 0; i < 2; ++i)
-    if (w + i * kWarps < a.T && lane < a.k) my_e[i] = sh.plan.e[(w + i * kWarps) * a.k + lane];
+    if (my_t + i * kWarps < a.T && lane < a.k) my_e[i] = sh.plan.e[(my_t + i * kWarps) * a.k + lane];
   static_assert(MOE_FEW_MAX_TOKENS <= 2 * kWarps, "a warp has at most two tokens' weights");
   __syncthreads();
 
@@ -915,18 +917,6 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       }
     }
   }
-  // the weights, while the grid finishes; the down units need them
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int t = w + i * kWarps;
-    if (t >= a.T || n_lists == 0) break;
-    const float wt = few_weight(a, t, my_e[i]);
-    if (lane < a.k) sh.pair_w[t * a.k + lane] = wt;
-    bool first = blockIdx.x == 0;  // the owner of the first list writes the routing out
-    for (int j = 1; j < n_lists; ++j) first |= sh.lists[j] == 0;
-    if (first) few_write_route(a, t, my_e[i], wt);
-  }
-
   // ---------------------------------------------------------------- every h is stored
   __syncthreads();
   if (n_lists == 0) {
@@ -937,7 +927,22 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     }
     return;
   }
-  for (int i = threadIdx.x; i < kWarps * MOE_FEW_MAX_TOKENS * 16; i += kStreamThreads) (&sh.y[0][0][0])[i] = 0.f;
+  if (threadIdx.x == 0) {
+    __threadfence();
+    atomicAdd(&a.counters[kFewDone], (uint32_t)n_lists);
+  }
+  // while the grid finishes: the weights, empty sums, and where the down entries' tokens lie
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int t = my_t + i * kWarps;
+    if (t >= a.T) break;
+    const float wt = few_weight(a, t, my_e[i]);
+    if (lane < a.k) sh.pair_w[t * a.k + lane] = wt;
+    bool first = blockIdx.x == 0;  // the owner of the first list writes the routing out
+    for (int j = 1; j < n_lists; ++j) first |= sh.lists[j] == 0;
+    if (first) few_write_route(a, t, my_e[i], wt);
+  }
+  for (int i = lane; i < a.T * 16; i += 32) (&sh.y[w][0][0])[i] = 0.f;
   for (int i = threadIdx.x; i < n_down * kDownTokens; i += kStreamThreads) {
     const uint32_t en = sh.down[i / kDownTokens];
     const int j = entry_start(en) + min(i % kDownTokens, entry_n(en) - 1);  // columns past the tokens are not used
@@ -945,8 +950,6 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         entry_e(en) == kSharedEntry ? (uint32_t)P * a.I + (uint32_t)j * a.Is : (uint32_t)(sh.pair[j] & 511) * a.I;
   }
   if (threadIdx.x == 0) {
-    __threadfence();
-    atomicAdd(&a.counters[kFewDone], (uint32_t)n_lists);
     const uint64_t t0 = global_timer_ns();
     for (;;) {
       uint32_t v;
