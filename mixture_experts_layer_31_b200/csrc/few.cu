@@ -410,13 +410,13 @@ __global__ void __launch_bounds__(kFewThreads) few_layer_kernel(const FewArgs a)
 // Measured, both launches, with what the bytes alone need at the copy rate of 6.55 TB/s:
 //   1 token   bf16, 2,304 wide, 256 experts of 2,048, 8 chosen, shared    55 us   39 us
 //   4 tokens  int8, the same layer                                        98 us   69 us
-//   16 tokens int8, the same layer                                       236 us  194 us
+//   16 tokens int8, the same layer                                       238 us  194 us
 //   1 token   int4, 2,048 wide, 128 experts of 768, 8 chosen              26 us    4 us
-//   16 tokens int4, the same layer                                       112 us   37 us
+//   16 tokens int4, the same layer                                       107 us   37 us
 // The first three are bound by HBM behind some 15 us of router, plan, first loads and barrier; one
 // int4 token by those alone.  Sixteen int4 tokens are bound by the instructions of the
 // products (a box of 2 KB takes some 250 of them, at 0.43 per cycle and scheduler with three
-// warps): gate and up 45 us, down 38, barrier and imbalance 12.
+// warps): gate and up 45 us, down 38, barrier and imbalance 10.
 
 constexpr int kWarps = 12;
 constexpr int kStreamThreads = 32 * kWarps;
@@ -1123,7 +1123,7 @@ cudaError_t launch_stream(FewArgs a, int num_sms, cudaStream_t s) {
   // instructions bound the stream; where the units are few, smaller teams leave warps without
   // work in the last round.  Measured (teams of 12, 3, 1): 1 token bf16 56, 57, 57 us and int4
   // 27, 28, 38 us; 4 tokens int8 128, 105, 118 us; 16 tokens int8 297, 240, 248 us and int4 138,
-  // 111, 124 us.  Down teams of 1 where 3 is chosen: within 1%.  The tokens' experts are not
+  // 111, 124 us (a step before the present one).  Down teams of 1 where 3 is chosen: within 1%.  The tokens' experts are not
   // known here: expect them to differ.
   const int touched = std::min(a.T * a.k, a.E);
   a.team = (int64_t)touched * (a.I / 16) >= 4LL * 4 * num_sms ? 3 : kWarps;
