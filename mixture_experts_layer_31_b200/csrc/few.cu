@@ -1123,8 +1123,8 @@ cudaError_t launch_stream(FewArgs a, int num_sms, cudaStream_t s) {
   // instructions bound the stream; where the units are few, smaller teams leave warps without
   // work in the last round.  Measured (teams of 12, 3, 1): 1 token bf16 56, 57, 57 us and int4
   // 27, 28, 38 us; 4 tokens int8 128, 105, 118 us; 16 tokens int8 297, 240, 248 us and int4 138,
-  // 111, 124 us (a step before the present one).  Down teams of 1 where 3 is chosen: within 1%.  The tokens' experts are not
-  // known here: expect them to differ.
+  // 111, 124 us (a step before the present one).  Down teams of 1 where 3 is chosen: within 1%.
+  // The tokens' experts are not known here: expect them to differ.
   const int touched = std::min(a.T * a.k, a.E);
   a.team = (int64_t)touched * (a.I / 16) >= 4LL * 4 * num_sms ? 3 : kWarps;
   a.down_team = touched >= 2 * kWarps ? 3 : kWarps;
