@@ -157,13 +157,13 @@ __device__ __forceinline__ void activate16(float (&v)[16], int act) {
   }
 }
 
-// 16 outputs of token m from column n0 on, in 16-byte pieces
+// 16 columns of the warp's 32 tokens, the lane's token m; the whole warp calls it
 template <bool GATED>
-__device__ __forceinline__ void finish16(const TcArgs& a, int split, int m, int n0, const uint32_t (&v)[16],
-                                         const uint32_t (&u)[16]) {
+__device__ __forceinline__ void output16(const TcArgs& a, int split, int m, int n0, const uint32_t (&v)[16],
+                                         const uint32_t (&u)[16], float* turn) {
   const LinearArgs& l = a.l;
   if (a.splits > 1) {
-    if (n0 >= a.np) return;
+    if (m >= l.M || n0 >= a.np) return;
     uint4* out = reinterpret_cast<uint4*>(a.partial + (((size_t)split * (GATED ? 2 : 1)) * l.M + m) * a.np + n0);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -172,6 +172,8 @@ __device__ __forceinline__ void finish16(const TcArgs& a, int split, int m, int 
     }
     return;
   }
+  const int last = l.N - 1 - n0;  // columns past the last one are computed with its scale and bias
+  if (last < 0) return;
   float y[16], g[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
@@ -181,13 +183,13 @@ __device__ __forceinline__ void finish16(const TcArgs& a, int split, int m, int 
   if (a.row_scales) {
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-      y[j] *= __ldg(l.s[0] + n0 + j);
-      if (GATED) g[j] *= __ldg(l.s[1] + n0 + j);
+      y[j] *= __ldg(l.s[0] + n0 + min(j, last));
+      if (GATED) g[j] *= __ldg(l.s[1] + n0 + min(j, last));
     }
   }
   if (l.b[0]) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) y[j] += __ldg(l.b[0] + n0 + j);
+    for (int j = 0; j < 16; ++j) y[j] += __ldg(l.b[0] + n0 + min(j, last));
   }
   if (l.act != MOE_ACT_NONE) {
     if (l.yfmt == MOE_X_BF16) activate16<true>(y, l.act);
@@ -196,11 +198,47 @@ __device__ __forceinline__ void finish16(const TcArgs& a, int split, int m, int 
   if constexpr (GATED) {
     if (l.b[1]) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) g[j] += __ldg(l.b[1] + n0 + j);
+      for (int j = 0; j < 16; ++j) g[j] += __ldg(l.b[1] + n0 + min(j, last));
     }
 #pragma unroll
     for (int j = 0; j < 16; ++j) y[j] *= g[j];
   }
+  if (!a.vec || last < 15) {
+    // rows of y that 16-byte pieces do not fit: turned from a row a lane to two rows at a time, 16
+    // columns each.  Pieces of sectors are what this costs: 1,172 x 1,472 -> 6,290, bf16, 48 us
+    // where 6,288 columns take 29 (and 71 with the activation behind the turn).
+    const int lane = lane_id(), c = lane & 15, first = m - lane + (lane >> 4);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) turn[lane * 17 + j] = y[j];
+    __syncwarp();
+    if (c <= last) {
+#pragma unroll 1
+      for (int r0 = 0; r0 < 32; r0 += 16) {
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = r0 + 2 * i, row = first + r;
+          o[i] = turn[(r + (lane >> 4)) * 17 + c];
+          if (l.residual && row < l.M) {
+            const size_t at = (size_t)row * l.ldr + n0 + c;
+            o[i] += l.yfmt == MOE_X_F32 ? static_cast<const float*>(l.residual)[at]
+                                        : bf16_to_f32(static_cast<const uint16_t*>(l.residual)[at]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int row = first + r0 + 2 * i;
+          if (row >= l.M) break;
+          const size_t at = (size_t)row * l.ldy + n0 + c;
+          if (l.yfmt == MOE_X_F32) static_cast<float*>(l.y)[at] = o[i];
+          else static_cast<uint16_t*>(l.y)[at] = f32_to_bf16(o[i]);
+        }
+      }
+    }
+    __syncwarp();
+    return;
+  }
+  if (m >= l.M) return;
   if (l.yfmt == MOE_X_BF16) {
     uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(l.y) + (size_t)m * l.ldy + n0);
     if (l.residual) {
@@ -230,34 +268,6 @@ __device__ __forceinline__ void finish16(const TcArgs& a, int split, int m, int 
       }
       out[j] = o;
     }
-  }
-}
-
-// 16 columns of the warp's 32 tokens, the lane's token m; the whole warp calls it
-template <bool GATED>
-__device__ __forceinline__ void output16(const TcArgs& a, int split, int m, int n0, const uint32_t (&v)[16],
-                                         const uint32_t (&u)[16], float* turn) {
-  const LinearArgs& l = a.l;
-  if (a.splits > 1 || (a.vec && n0 + 16 <= l.N)) {
-    if (m < l.M) finish16<GATED>(a, split, m, n0, v, u);
-    return;
-  }
-  // rows of y that 16-byte pieces do not fit: turned from a row a lane to some rows at a time, 16
-  // columns each (gated: 8, with their up sums beside them)
-  constexpr int kWide = GATED ? 8 : 16;
-  const int lane = lane_id();
-#pragma unroll
-  for (int p = 0; p < 16 / kWide; ++p) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      turn[lane * 17 + j] = __uint_as_float(!GATED ? v[j] : (j < 8 ? v[(8 * p + j) & 15] : u[(8 * p + j - 8) & 15]));
-    __syncwarp();
-#pragma unroll 1
-    for (int r0 = 0; r0 < 32; r0 += 32 / kWide) {
-      const int r = r0 + lane / kWide, c = lane % kWide, row = m - lane + r, n = n0 + p * kWide + c;
-      if (row < l.M && n < l.N) linear_finish(l, a.row_scales, row, n, turn[r * 17 + c], turn[r * 17 + (GATED ? 8 + c : c)]);
-    }
-    __syncwarp();
   }
 }
 // one copy of it for a loop that is unrolled: eight copies' way into the instruction cache took
@@ -389,7 +399,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const int q = w & 3, group = (w - 4) >> 2;  // lane quarter; half of the columns
     constexpr int kCols = GATED ? kTileN / 4 : kTileN / 2;  // outputs of a group
     const int outs = GATED ? kRows : 2 * kRows;             // outputs of a tile
-    const LinearArgs& l = a.l;
     bool dead = false;
     uint32_t n = 0;
     for (int t = pair; t < tiles && !dead; t += pairs) {
