@@ -29,7 +29,8 @@
 // Quantised weights are widened to bf16 in the workspace first: int8 codes exactly, with the row
 // scale left for the epilogue, int4 as q s rounded once where y is bf16 (half a step of bf16 per
 // weight, as the routed layer's tensor-core path has it: measured against 64 bits 2.2 x 10^-3
-// where y's own rounding alone leaves 1.7 x 10^-3), in three parts where y is fp32.
+// where y's own rounding alone leaves 1.7 x 10^-3), in two parts where two such projections are
+// multiplied (one part left 2.7 x 10^-3), in three parts where y is fp32.
 // The pass costs 3 bytes or 2.6 per weight, most of it in L2, against 2 M operations per
 // weight.
 //
@@ -67,7 +68,7 @@ struct TcArgs {
   int row_scales;       // int8: the epilogue scales the sums
   int mt, nt, splits;   // tiles of 256 tokens, of 256 (gated: 128) outputs; parts of the reduction
   int ksteps, segment;  // columns steps of the reduction; of one accumulator
-  int xparts, wparts;   // bf16 parts of x and of W: 1, or 3 of an fp32 operand (its rows follow one another)
+  int xparts, wparts;   // bf16 parts of x and of W, whose rows follow one another: 1, 3 of an fp32 operand, 2 of int4
   int vec;              // y and residual rows in 16-byte pieces
   float* partial;       // splits > 1: [splits][1 or 2][M][np]
   int np;               // N rounded up to 16
@@ -526,11 +527,11 @@ __device__ __forceinline__ float int4_value(uint32_t codes, int j, float s) {
   return (__uint_as_float(v) - 8388616.f) * s;
 }
 
-// Each row to its three parts, [3][rows][pitch], zero between cols and pitch.  WF: fp32, or int4
+// Each row to its two or three parts, [parts][rows][pitch], zero between cols and pitch.  WF: fp32, or int4
 // codes times their block scales in fp32.
 template <int WF>
 __device__ __forceinline__ void split_rows(const void* __restrict__ W, const float* __restrict__ s, long long ld, int rows,
-                                           int cols, int pitch, uint16_t* __restrict__ out) {
+                                           int cols, int pitch, int parts, uint16_t* __restrict__ out) {
   const int eights = pitch / 8;
   const size_t n = (size_t)rows * eights, plane = (size_t)rows * pitch;
   constexpr int kAtOnce = kItems / 2;
@@ -567,10 +568,12 @@ __device__ __forceinline__ void split_rows(const void* __restrict__ W, const flo
 #pragma unroll
       for (int j = 0; j < 8; ++j) split3(v[k][j], p[j]);
 #pragma unroll
-      for (int q = 0; q < 3; ++q)  // pieces follow one another in a plane: row r, column c is piece i
+      for (int q = 0; q < 3; ++q) {  // pieces follow one another in a plane: row r, column c is piece i
+        if (q >= parts) break;
         *reinterpret_cast<uint4*>(out + q * plane + 8 * i) =
             make_uint4(p[0][q] | (uint32_t)p[1][q] << 16, p[2][q] | (uint32_t)p[3][q] << 16, p[4][q] | (uint32_t)p[5][q] << 16,
                        p[6][q] | (uint32_t)p[7][q] << 16);
+      }
     }
   }
 }
@@ -621,6 +624,7 @@ struct Layouts {
   const float* s[3];
   uint16_t* to[3];
   int x, rows_w, rows_x, K, pitch;  // which one holds the tokens, -1 for none
+  int wparts;
   long long ldx;
 };
 
@@ -629,8 +633,8 @@ __global__ void __launch_bounds__(256) linear_layout_kernel(const __grid_constan
   pdl_wait();
   pdl_trigger();
   const int j = blockIdx.y;
-  if (j == p.x) split_rows<MOE_W_F32>(p.from[j], nullptr, p.ldx, p.rows_x, p.K, p.pitch, p.to[j]);
-  else if constexpr (SPLIT) split_rows<WF>(p.from[j], p.s[j], p.K, p.rows_w, p.K, p.pitch, p.to[j]);
+  if (j == p.x) split_rows<MOE_W_F32>(p.from[j], nullptr, p.ldx, p.rows_x, p.K, p.pitch, 3, p.to[j]);
+  else if constexpr (SPLIT) split_rows<WF>(p.from[j], p.s[j], p.K, p.rows_w, p.K, p.pitch, p.wparts, p.to[j]);
   else if constexpr (WF != MOE_W_F32) widen_values<WF>(p.from[j], p.s[j], (size_t)p.rows_w * p.K / 8, p.to[j]);
 }
 
@@ -650,8 +654,8 @@ TcLayout tc_layout(const moe_linear_desc& d, int M) {
   const bool gated = d.W_up != nullptr, int4 = d.wfmt == MOE_W_INT4_B32 || d.wfmt == MOE_W_INT4_B128;
   const int outs = gated ? kRows : 2 * kRows, sides = gated ? 2 : 1;
   t.xparts = d.xfmt == MOE_X_F32 ? 3 : 1;
-  // an fp32 output keeps what a rounded q s would lose
-  t.wparts = d.wfmt == MOE_W_F32 || (int4 && (d.xfmt == MOE_X_F32 || d.yfmt == MOE_X_F32)) ? 3 : 1;
+  // an fp32 output keeps what a rounded q s would lose, and so, in part, does a product of two
+  t.wparts = d.wfmt == MOE_W_F32 || (int4 && (d.xfmt == MOE_X_F32 || d.yfmt == MOE_X_F32)) ? 3 : (int4 && gated ? 2 : 1);
   t.mt = (M + 2 * kRows - 1) / (2 * kRows);
   t.nt = (d.N + outs - 1) / outs;
   t.ksteps = (d.K + kK - 1) / kK;
@@ -703,7 +707,7 @@ cudaError_t launch_linear_layouts(const moe_linear_desc& d, const LinearArgs& a,
   const TcLayout t = tc_layout(d, a.M);
   char* ws = static_cast<char*>(workspace);
   Layouts p = {};
-  p.x = -1, p.rows_w = d.N, p.rows_x = a.M, p.K = d.K, p.pitch = t.pitch, p.ldx = a.ldx;
+  p.x = -1, p.rows_w = d.N, p.rows_x = a.M, p.K = d.K, p.pitch = t.pitch, p.wparts = t.wparts, p.ldx = a.ldx;
   int n = 0;
   size_t most = 0;
   auto add = [&](const void* from, const float* sc, size_t to, size_t rows) {
@@ -719,7 +723,7 @@ cudaError_t launch_linear_layouts(const moe_linear_desc& d, const LinearArgs& a,
   const size_t blocks = (most / 8 + 256 * kItems - 1) / (256 * kItems);
   const dim3 grid((unsigned)std::min<size_t>(blocks, (size_t)num_sms * 8), n);
   auto go = [&](auto kernel) { return launch_k(kernel, grid, dim3(256), 0, s, p); };
-  const bool split = t.wparts == 3;
+  const bool split = t.wparts > 1;
   switch (d.wfmt) {
     case MOE_W_INT8_ROW: return go(linear_layout_kernel<MOE_W_INT8_ROW, false>);
     case MOE_W_INT4_B32:
@@ -755,7 +759,7 @@ cudaError_t launch_linear_tc(const moe_linear_desc& d, const LinearArgs& a, void
                             t.xparts == 3 ? (uint64_t)t.pitch * 2 : (uint64_t)a.ldx * 2, kK, kRows, CU_TENSOR_MAP_SWIZZLE_128B);
   for (int i = 0; i < (gated ? 2 : 1) && e == cudaSuccess; ++i)
     e = make_tmap(&mw[i], t.w_copy ? ws + t.w[i] : a.W[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (uint64_t)d.K,
-                  (uint64_t)d.N * t.wparts, t.wparts == 3 ? (uint64_t)t.pitch * 2 : (uint64_t)d.K * 2, kK, kRows,
+                  (uint64_t)d.N * t.wparts, t.wparts > 1 ? (uint64_t)t.pitch * 2 : (uint64_t)d.K * 2, kK, kRows,
                   CU_TENSOR_MAP_SWIZZLE_128B);
   if (!gated) mw[1] = mw[0];
   // a split that is one segment long needs no segments

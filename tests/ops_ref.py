@@ -59,11 +59,12 @@ def sum_error(n, magnitude):
     return (n + STEPS) * U * magnitude
 
 
-def widened_error(wfmt, x_is_bf16, magnitude, exact_int4):
-    """int4 weights on the tensor cores are multiplied by their scale and rounded to bf16 where
-    the batch is large (half a step of each weight); elsewhere every code is exact."""
-    if wfmt in ("int4", "int4b128") and x_is_bf16 and not exact_int4:
-        return HALF[torch.bfloat16] * magnitude
+def widened_error(wfmt, x_is_bf16, magnitude, int4_parts):
+    """int4 weights on the tensor cores are multiplied by their scale and rounded to bf16 where the
+    batch is large (half a step of each weight), or to two bf16 parts (what the first leaves is
+    half a step at most, and half a step of that is left out); 0 parts: every code is exact."""
+    if wfmt in ("int4", "int4b128") and x_is_bf16 and int4_parts:
+        return HALF[torch.bfloat16] ** int4_parts * magnitude
     return 0.0
 
 
@@ -75,7 +76,7 @@ def digit_error(x, Wd, wfmt):
     return 2.0 ** -30 * x.double().abs().amax(1, keepdim=True) * Wd.abs().sum(1)[None, :]
 
 
-def linear(x, W, s_b, up=None, act_name="none", residual=None, y_dtype=torch.float32, wfmt="f32", exact_int4=True):
+def linear(x, W, s_b, up=None, act_name="none", residual=None, y_dtype=torch.float32, wfmt="f32", int4_parts=0):
     """(reference, bound) of y = act(W x + b) [* (W_up x + b_up)] + residual; W, W_up float64
     [N, K]; s_b, and up's second entry: fp64 biases or None."""
     xd = x.double()
@@ -84,7 +85,7 @@ def linear(x, W, s_b, up=None, act_name="none", residual=None, y_dtype=torch.flo
     def product(Wd, b):
         v = xd @ Wd.T
         m = xd.abs() @ Wd.abs().T
-        e = sum_error(Wd.shape[1], m) + widened_error(wfmt, bf, m, exact_int4) + digit_error(x, Wd, wfmt)
+        e = sum_error(Wd.shape[1], m) + widened_error(wfmt, bf, m, int4_parts) + digit_error(x, Wd, wfmt)
         if b is not None:
             v = v + b
             e = e + 2 * U * (v.abs() + b.abs())

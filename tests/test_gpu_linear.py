@@ -41,10 +41,10 @@ class Product:
 
     def compare(self, x, y, residual=None, what=""):
         # int4 weights are widened exactly for up to 40 tokens and for fp32 outputs; else each is rounded
-        # to bf16 once, which is off by half a step of bf16 at most (moe_linear)
+        # to bf16 once, which is off by half a step of bf16 at most, or kept in two parts (moe_linear)
         exact = x.shape[0] <= 40 or self.y_dtype == torch.float32
         want, bound = ref.linear(x, self.W, self.b, None if self.Wu is None else (self.Wu, self.bu), self.act, residual,
-                                 self.y_dtype, self.wfmt, exact)
+                                 self.y_dtype, self.wfmt, 0 if exact else (1 if self.Wu is None else 2))
         ref.check(y, want, bound, what)
 
     def run(self, M, residual=False):
