@@ -527,11 +527,34 @@ __device__ __forceinline__ float int4_value(uint32_t codes, int j, float s) {
   return (__uint_as_float(v) - 8388616.f) * s;
 }
 
-// Each row to its two or three parts, [parts][rows][pitch], zero between cols and pitch.  WF: fp32, or int4
-// codes times their block scales in fp32.
-template <int WF>
-__device__ __forceinline__ void split_rows(const void* __restrict__ W, const float* __restrict__ s, long long ld, int rows,
-                                           int cols, int pitch, int parts, uint16_t* __restrict__ out) {
+// 8 values in PARTS bf16 parts, `plane` apart
+template <int PARTS>
+__device__ __forceinline__ void store_parts(const float (&v)[8], uint16_t* out, size_t plane) {
+  if constexpr (PARTS == 3) {
+    uint16_t p[8][3];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) split3(v[j], p[j]);
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+      *reinterpret_cast<uint4*>(out + q * plane) =
+          make_uint4(p[0][q] | (uint32_t)p[1][q] << 16, p[2][q] | (uint32_t)p[3][q] << 16, p[4][q] | (uint32_t)p[5][q] << 16,
+                     p[6][q] | (uint32_t)p[7][q] << 16);
+  } else {
+    uint32_t h[4], m[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      h[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+      const float h0 = bf16_to_f32(h[j] & 0xFFFFu), h1 = __uint_as_float(h[j] & 0xFFFF0000u);
+      if (PARTS == 2) m[j] = pack_bf16x2(isfinite(h0) ? v[2 * j] - h0 : 0.f, isfinite(h1) ? v[2 * j + 1] - h1 : 0.f);
+    }
+    *reinterpret_cast<uint4*>(out) = make_uint4(h[0], h[1], h[2], h[3]);
+    if (PARTS == 2) *reinterpret_cast<uint4*>(out + plane) = make_uint4(m[0], m[1], m[2], m[3]);
+  }
+}
+
+// fp32 rows to their three parts, [3][rows][pitch], zero between cols and pitch.
+__device__ __forceinline__ void split_rows(const float* __restrict__ W, long long ld, int rows, int cols, int pitch,
+                                           uint16_t* __restrict__ out) {
   const int eights = pitch / 8;
   const size_t n = (size_t)rows * eights, plane = (size_t)rows * pitch;
   constexpr int kAtOnce = kItems / 2;
@@ -540,46 +563,30 @@ __device__ __forceinline__ void split_rows(const void* __restrict__ W, const flo
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
       const size_t i = i0 + 256 * k;
-      const int r = (int)(i / eights), c = (int)(i - (size_t)r * eights) * 8;
+      const int r = (int)(n >> 32 ? i / (size_t)eights : (uint32_t)i / (uint32_t)eights);
+      const int c = (int)(i - (size_t)r * eights) * 8;
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[k][j] = 0.f;
       if (i >= n || c >= cols) continue;
-      if constexpr (WF == MOE_W_F32) {  // cols is a multiple of 4
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(W) + (size_t)r * ld + c);
-        const float4 a = __ldg(p);
-        v[k][0] = a.x, v[k][1] = a.y, v[k][2] = a.z, v[k][3] = a.w;
-        if (c + 4 < cols) {
-          const float4 b = __ldg(p + 1);
-          v[k][4] = b.x, v[k][5] = b.y, v[k][6] = b.z, v[k][7] = b.w;
-        }
-      } else {
-        constexpr int kShift = WF == MOE_W_INT4_B32 ? 5 : 7;
-        const uint32_t q = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(W) + ((size_t)r * cols + c) / 2));
-        const float scale = __ldg(s + (size_t)r * (cols >> kShift) + (c >> kShift));
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[k][j] = int4_value(q, j, scale);
+      const float4* p = reinterpret_cast<const float4*>(W + (size_t)r * ld + c);  // cols is a multiple of 4
+      const float4 a = __ldg(p);
+      v[k][0] = a.x, v[k][1] = a.y, v[k][2] = a.z, v[k][3] = a.w;
+      if (c + 4 < cols) {
+        const float4 b = __ldg(p + 1);
+        v[k][4] = b.x, v[k][5] = b.y, v[k][6] = b.z, v[k][7] = b.w;
       }
     }
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
       const size_t i = i0 + 256 * k;
       if (i >= n) break;
-      uint16_t p[8][3];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) split3(v[k][j], p[j]);
-#pragma unroll
-      for (int q = 0; q < 3; ++q) {  // pieces follow one another in a plane: row r, column c is piece i
-        if (q >= parts) break;
-        *reinterpret_cast<uint4*>(out + q * plane + 8 * i) =
-            make_uint4(p[0][q] | (uint32_t)p[1][q] << 16, p[2][q] | (uint32_t)p[3][q] << 16, p[4][q] | (uint32_t)p[5][q] << 16,
-                       p[6][q] | (uint32_t)p[7][q] << 16);
-      }
+      store_parts<3>(v[k], out + 8 * i, plane);  // pieces follow one another in a plane: row r, column c is piece i
     }
   }
 }
 
-// stored weights to bf16
-template <int WF>
+// stored weights to bf16: int8 codes, or int4 codes times their block scales in fp32 in PARTS parts
+template <int WF, int PARTS>
 __device__ __forceinline__ void widen_values(const void* __restrict__ W, const float* __restrict__ s, size_t n8,
                                              uint16_t* __restrict__ out) {
   for (size_t i0 = (size_t)blockIdx.x * 256 * kItems + threadIdx.x; i0 < n8; i0 += (size_t)gridDim.x * 256 * kItems) {
@@ -601,19 +608,20 @@ __device__ __forceinline__ void widen_values(const void* __restrict__ W, const f
     for (int k = 0; k < kItems; ++k) {
       const size_t i = i0 + 256 * k;
       if (i >= n8) break;
-      uint32_t o[4];
       if constexpr (WF == MOE_W_INT8_ROW) {
+        uint32_t o[4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint32_t w = h ? q[k].y : q[k].x, even = stream::widen_int8(w), odd = stream::widen_int8(w >> 8);
           o[2 * h] = __byte_perm(even, odd, 0x5410), o[2 * h + 1] = __byte_perm(even, odd, 0x7632);
         }
+        *reinterpret_cast<uint4*>(out + 8 * i) = make_uint4(o[0], o[1], o[2], o[3]);
       } else {
+        float v[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          o[j] = pack_bf16x2(int4_value(q[k].x, 2 * j, scale[k]), int4_value(q[k].x, 2 * j + 1, scale[k]));
+        for (int j = 0; j < 8; ++j) v[j] = int4_value(q[k].x, j, scale[k]);
+        store_parts<PARTS>(v, out + 8 * i, 8 * n8);
       }
-      *reinterpret_cast<uint4*>(out + 8 * i) = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
 }
@@ -624,18 +632,17 @@ struct Layouts {
   const float* s[3];
   uint16_t* to[3];
   int x, rows_w, rows_x, K, pitch;  // which one holds the tokens, -1 for none
-  int wparts;
   long long ldx;
 };
 
-template <int WF, bool SPLIT>
+template <int WF, int PARTS>
 __global__ void __launch_bounds__(256) linear_layout_kernel(const __grid_constant__ Layouts p) {
   pdl_wait();
   pdl_trigger();
   const int j = blockIdx.y;
-  if (j == p.x) split_rows<MOE_W_F32>(p.from[j], nullptr, p.ldx, p.rows_x, p.K, p.pitch, 3, p.to[j]);
-  else if constexpr (SPLIT) split_rows<WF>(p.from[j], p.s[j], p.K, p.rows_w, p.K, p.pitch, p.wparts, p.to[j]);
-  else if constexpr (WF != MOE_W_F32) widen_values<WF>(p.from[j], p.s[j], (size_t)p.rows_w * p.K / 8, p.to[j]);
+  if (j == p.x) split_rows(static_cast<const float*>(p.from[j]), p.ldx, p.rows_x, p.K, p.pitch, p.to[j]);
+  else if constexpr (WF == MOE_W_F32) split_rows(static_cast<const float*>(p.from[j]), p.K, p.rows_w, p.K, p.pitch, p.to[j]);
+  else widen_values<WF, PARTS>(p.from[j], p.s[j], (size_t)p.rows_w * p.K / 8, p.to[j]);
 }
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -707,7 +714,7 @@ cudaError_t launch_linear_layouts(const moe_linear_desc& d, const LinearArgs& a,
   const TcLayout t = tc_layout(d, a.M);
   char* ws = static_cast<char*>(workspace);
   Layouts p = {};
-  p.x = -1, p.rows_w = d.N, p.rows_x = a.M, p.K = d.K, p.pitch = t.pitch, p.wparts = t.wparts, p.ldx = a.ldx;
+  p.x = -1, p.rows_w = d.N, p.rows_x = a.M, p.K = d.K, p.pitch = t.pitch, p.ldx = a.ldx;
   int n = 0;
   size_t most = 0;
   auto add = [&](const void* from, const float* sc, size_t to, size_t rows) {
@@ -723,14 +730,15 @@ cudaError_t launch_linear_layouts(const moe_linear_desc& d, const LinearArgs& a,
   const size_t blocks = (most / 8 + 256 * kItems - 1) / (256 * kItems);
   const dim3 grid((unsigned)std::min<size_t>(blocks, (size_t)num_sms * 8), n);
   auto go = [&](auto kernel) { return launch_k(kernel, grid, dim3(256), 0, s, p); };
-  const bool split = t.wparts > 1;
+  auto int4 = [&](auto format) {
+    constexpr int WF = decltype(format)::value;
+    return t.wparts == 1 ? go(linear_layout_kernel<WF, 1>) : (t.wparts == 2 ? go(linear_layout_kernel<WF, 2>) : go(linear_layout_kernel<WF, 3>));
+  };
   switch (d.wfmt) {
-    case MOE_W_INT8_ROW: return go(linear_layout_kernel<MOE_W_INT8_ROW, false>);
-    case MOE_W_INT4_B32:
-      return split ? go(linear_layout_kernel<MOE_W_INT4_B32, true>) : go(linear_layout_kernel<MOE_W_INT4_B32, false>);
-    case MOE_W_INT4_B128:
-      return split ? go(linear_layout_kernel<MOE_W_INT4_B128, true>) : go(linear_layout_kernel<MOE_W_INT4_B128, false>);
-    default: return go(linear_layout_kernel<MOE_W_F32, true>);  // fp32 weights, or fp32 tokens alone
+    case MOE_W_INT8_ROW: return go(linear_layout_kernel<MOE_W_INT8_ROW, 1>);
+    case MOE_W_INT4_B32: return int4(std::integral_constant<int, MOE_W_INT4_B32>());
+    case MOE_W_INT4_B128: return int4(std::integral_constant<int, MOE_W_INT4_B128>());
+    default: return go(linear_layout_kernel<MOE_W_F32, 3>);  // fp32 weights, or fp32 tokens alone
   }
 }
 
