@@ -284,8 +284,10 @@ MOE_API moe_status moe_forward_block(const moe_desc* d, const moe_shared_expert*
  *     bits, and a token that holds an infinity or NaN gives NaN in its whole row of y.
  *   - d->path is not read.
  * The workspace (moe_few_workspace_size bytes, 256-byte aligned) needs no initial state;
- * calls on one stream may share it, calls that can overlap must not.  Asynchronous on
- * `stream`, no allocation, capturable.
+ * calls on one stream may share it, calls that can overlap must not.  A call is two launches:
+ * a host thread must not enqueue one while another thread is inside a call with the same
+ * workspace, even on the same stream (the second thread's launches could come between the
+ * first one's).  Asynchronous on `stream`, no allocation, capturable.
  */
 #define MOE_FEW_MAX_TOKENS 16
 MOE_API moe_status moe_few_workspace_size(const moe_desc* d, const moe_shared_expert* shared, int32_t T,
@@ -325,8 +327,9 @@ MOE_API moe_status moe_few_forward(const moe_desc* d, const moe_shared_expert* s
  * exact for up to 40 tokens (of bf16; 48 where K > 4096) and wherever y is fp32; beyond, with
  * bf16 tokens and bf16 y, each is rounded to bf16 once (gated: kept to 16 bits).
  * The workspace is as for moe_forward: moe_linear_workspace_size bytes for this very M (fewer
- * rows may need more; may be 0, then it may be NULL), 256-byte aligned, no initial state needed, shared by the calls of one
- * stream only.  Asynchronous on `stream`, no allocation, capturable.
+ * rows may need more; may be 0, then it may be NULL), 256-byte aligned, no initial state
+ * needed, shared by the calls of one stream only, and of one host thread at a time (a call is
+ * up to three launches).  Asynchronous on `stream`, no allocation, capturable.
  */
 typedef struct {
   int32_t K, N;

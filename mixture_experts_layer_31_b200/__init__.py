@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from typing import Optional, Tuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -369,6 +370,7 @@ class MoELayer:
         self._bws = None
         self._bws_T = -1
         self._few_ws = {}
+        self._few_lock = threading.Lock()
 
     @property
     def x_dtype(self):
@@ -451,8 +453,9 @@ class MoELayer:
         return y
 
     def few_workspace(self, T: int, stream: int = 0):
-        """The workspace of few() calls on one stream (they run in order and share it).  A call
-        that is being captured gets one of its own, which lives in its graph's memory."""
+        """The workspace of few() calls on one stream (they run in order and share it, few() lets one
+        host thread at a time put its launches there).  A call that is being captured gets one
+        of its own, which lives in its graph's memory."""
         ws = self._few_ws.get(stream)
         capturing = _capturing(self.torch)
         if capturing or ws is None or ws[0] < T:
@@ -489,9 +492,11 @@ class MoELayer:
                      "residual must be a contiguous %s tensor [%d, %d] on x's device" % (dtype, T, H))
             r = residual.data_ptr()
         stream = _raw_stream(torch, device)
-        ws = self.few_workspace(T, stream)
-        st = lib().moe_few_forward(ctypes.byref(d), None if self.shared is None else ctypes.byref(self.shared), x.data_ptr(),
-                                   T, idx.data_ptr(), w.data_ptr(), r, y.data_ptr(), ws.data_ptr(), ws.numel(), stream)
+        with self._few_lock:  # the call's launches must follow one another on the stream
+            ws = self.few_workspace(T, stream)
+            st = lib().moe_few_forward(ctypes.byref(d), None if self.shared is None else ctypes.byref(self.shared),
+                                       x.data_ptr(), T, idx.data_ptr(), w.data_ptr(), r, y.data_ptr(), ws.data_ptr(),
+                                       ws.numel(), stream)
         if st:
             _check(st)
         return out
@@ -534,10 +539,12 @@ class Linear:
         self.y_dtype = torch.bfloat16 if d.yfmt == MOE_X_BF16 else torch.float32
         self._ws = {}
         self._need = {}  # workspace bytes by M
+        self._lock = threading.Lock()
 
     def workspace(self, M: int, stream: int = 0):
-        """The workspace of the calls on one stream (they run in order and share it).  A call that
-        is being captured gets one of its own, which lives in its graph's memory."""
+        """The workspace of the calls on one stream (they run in order and share it, and one host
+        thread at a time puts its launches there).  A call that is being captured gets one of
+        its own, which lives in its graph's memory."""
         n = self._need.get(M)
         if n is None:
             n = self._need[M] = moe_linear_workspace_size(self.desc, M)
@@ -572,9 +579,10 @@ class Linear:
                      "residual must be a %s tensor [%d, %d] with contiguous rows on x's device" % (dtype, M, N))
             r, ldr = residual.data_ptr(), residual.stride(0) if M > 1 else N
         stream = _raw_stream(torch, device)
-        ws = self.workspace(M, stream)
-        st = lib().moe_linear(ctypes.byref(d), x.data_ptr(), x.stride(0) if M > 1 else K, M, r, ldr, y.data_ptr(),
-                              y.stride(0) if M > 1 else N, ws.data_ptr(), ws.numel(), stream)
+        with self._lock:  # the call's launches must follow one another on the stream
+            ws = self.workspace(M, stream)
+            st = lib().moe_linear(ctypes.byref(d), x.data_ptr(), x.stride(0) if M > 1 else K, M, r, ldr, y.data_ptr(),
+                                  y.stride(0) if M > 1 else N, ws.data_ptr(), ws.numel(), stream)
         if st:
             _check(st)
         return y

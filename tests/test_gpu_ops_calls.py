@@ -1,0 +1,61 @@
+"""How calls of the few-token layer and the dense product get on with one another: host threads on
+one stream, programmatic launches, CTAs that start late."""
+import threading
+
+import pytest
+import torch
+
+import mixture_experts_layer_31_b200 as moe
+from test_gpu_few import Layer
+from test_gpu_linear import Product
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _clear_flags():
+    moe.moe_device_flags(clear=True)
+    yield
+    assert moe.moe_device_flags(clear=True) == 0
+
+
+def _same_in_threads(call, inputs, rounds):
+    """Each input from a thread of its own, all on one stream, gives what it gives alone."""
+    want = [[t.clone() for t in call(x)] for x in inputs]
+    torch.cuda.synchronize()
+    got, errors, start = [[] for _ in inputs], [], threading.Barrier(len(inputs))
+
+    def work(n):
+        try:
+            start.wait()
+            for _ in range(rounds):
+                got[n].append(call(inputs[n]))
+        except Exception as e:  # shown by the assertion below
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(n,)) for n in range(len(inputs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for outs, w in zip(got, want):
+        assert len(outs) == rounds
+        assert all(torch.equal(a, b) for out in outs for a, b in zip(out, w))
+
+
+@pytest.mark.parametrize("wfmt,xfmt", [("int8", "bf16"), ("bf16", "bf16"), ("f32", "f32")])
+def test_few_from_several_threads_on_one_stream(wfmt, xfmt):
+    layer = Layer(E=32, k=4, H=512, I=256, wfmt=wfmt, xfmt=xfmt)
+    _same_in_threads(lambda x: layer.dev.few(x), [layer.x(4, 80 + n).cuda() for n in range(4)], 60)
+
+
+@pytest.mark.parametrize("K,N,wfmt,xfmt,M", [
+    (4608, 80, "int8", "bf16", 5),      # digits, product
+    (2048, 320, "int8", "bf16", 130),   # widened weights, product, sum of the reduction's parts
+    (1024, 320, "f32", "f32", 50),      # operands in parts, product, sum
+])
+def test_linear_from_several_threads_on_one_stream(K, N, wfmt, xfmt, M):
+    p = Product(K, N, wfmt, xfmt)
+    _same_in_threads(lambda x: [p.dev(x)], [p.x(M, 90 + n).cuda() for n in range(4)], 60)
