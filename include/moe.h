@@ -323,7 +323,8 @@ MOE_API moe_status moe_few_forward(const moe_desc* d, const moe_shared_expert* s
  * Sums are fp32 (integers where a few bf16 tokens meet int8 or int4 weights: the token is
  * taken as integers of 31 bits relative to its largest magnitude, and one that holds an
  * infinity or NaN gives NaN in its whole row of y).  fp32 weights and tokens are multiplied in
- * fp32, for more tokens in three bf16 parts each that hold every bit.  int4 weights are
+ * fp32, for more tokens in three bf16 parts each that hold every bit of magnitudes from 2^-100
+ * up; infinities are infinities there too.  int4 weights are
  * exact for up to 40 tokens (of bf16; 48 where K > 4096) and wherever y is fp32; beyond, with
  * bf16 tokens and bf16 y, each is rounded to bf16 once (gated: kept to 16 bits).
  * The workspace is as for moe_forward: moe_linear_workspace_size bytes for this very M (fewer

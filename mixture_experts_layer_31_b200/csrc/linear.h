@@ -60,6 +60,52 @@ __device__ __forceinline__ void linear_finish(const LinearArgs& a, bool row_scal
   }
 }
 
+// 8 stored weights of row r from column c on (c a multiple of 8, or of 4 with 4 columns left)
+template <int WF>
+__device__ __forceinline__ void weights8(const void* W, const float* s, size_t r, int c, int K, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = 0.f;
+  if constexpr (WF == MOE_W_F32) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(W) + r * K + c);
+    const float4 a = __ldg(p);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    if (c + 4 < K) {
+      const float4 b = __ldg(p + 1);
+      v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+  } else if constexpr (WF == MOE_W_BF16) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(W) + r * K + c));
+    const uint32_t word[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[2 * j] = bf16_to_f32(word[j] & 0xFFFFu), v[2 * j + 1] = __uint_as_float(word[j] & 0xFFFF0000u);
+  } else if constexpr (WF == MOE_W_INT8_ROW) {
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const int8_t*>(W) + r * K + c));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = (float)(int8_t)((j < 4 ? u.x : u.y) >> (8 * (j & 3)));
+  } else {
+    constexpr int kShift = WF == MOE_W_INT4_B32 ? 5 : 7;
+    const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(W) + (r * K + c) / 2));
+    const float scale = __ldg(s + r * (K >> kShift) + (c >> kShift));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = (float)((int)(u << (28 - 4 * j)) >> 28) * scale;
+  }
+}
+
+// 8 columns of a token
+template <int XF>
+__device__ __forceinline__ void token8(const void* x, size_t at, bool all, float (&v)[8]) {
+  if constexpr (XF == MOE_X_F32) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
+    const float4 a = __ldg(p), b = all ? __ldg(p + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at));
+    const uint32_t word[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[2 * j] = bf16_to_f32(word[j] & 0xFFFFu), v[2 * j + 1] = __uint_as_float(word[j] & 0xFFFF0000u);
+  }
+}
+
 bool linear_stream_ok(const moe_linear_desc& d, int M);
 bool linear_stream_digits(const moe_linear_desc& d, int M);        // the tokens are taken as digits
 bool linear_stream_digits_first(const moe_linear_desc& d, int M);  // which a launch before it makes

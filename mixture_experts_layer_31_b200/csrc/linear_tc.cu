@@ -20,7 +20,9 @@
 // significant bits each, exactly: the products of parts that matter to 24 bits (six of two
 // fp32 operands, three where one is exact in bf16) are summed, the small ones first; what is
 // left out is below 2^-23 of each product.  That is six times the operations of a bf16
-// product and still several times the rate of fp32 multiply-adds.
+// product and still several times the rate of fp32 multiply-adds.  An infinity has the parts
+// (inf, 0, 0), and infinity times another operand's zero or negative part is NaN where the product
+// is infinite: sums of parts that come out NaN are formed again in fp32 from the operands themselves.
 // The tensor core's own additions cut off: over 2,304 columns in one accumulator the result
 // came out 2 x 10^-6 too small (of its mean magnitude), over 9,216 columns 4 x 10^-6.  Where the
 // output is fp32, the accumulator is therefore drained every kSegment stages and the drained
@@ -69,6 +71,8 @@ struct TcArgs {
   int mt, nt, splits;   // tiles of 256 tokens, of 256 (gated: 128) outputs; parts of the reduction
   int ksteps, segment;  // columns steps of the reduction; of one accumulator
   int xparts, wparts;   // bf16 parts of x and of W, whose rows follow one another: 1, 3 of an fp32 operand, 2 of int4
+  int xfmt, wfmt;       // of the operands as they are stored
+  int again;            // products of parts: sums that are NaN are formed again
   int vec;              // y and residual rows in 16-byte pieces
   float* partial;       // splits > 1: [splits][1 or 2][M][np]
   int np;               // N rounded up to 16
@@ -140,6 +144,65 @@ __device__ __forceinline__ Tile tile_of(const TcArgs& a, int t) {
   r.m = g * 8 + in % size;
   r.n = in / size;
   return r;
+}
+
+// Columns c, c + step, ... (8 from each on) of the product of token m and row n of W (side 0) or W_up, in
+// fp32 multiply-adds; int8 codes without their row's scale, as the accumulators have them.
+__device__ __noinline__ float sum_again(const TcArgs& a, int side, int m, int n, int c, int step) {
+  const LinearArgs& l = a.l;
+  float acc = 0.f;
+#pragma unroll 2
+  for (; c < l.K && acc == acc; c += step) {  // a NaN stays one
+    float w[8], x[8];
+    switch (a.wfmt) {
+      case MOE_W_F32: weights8<MOE_W_F32>(l.W[side], l.s[side], n, c, l.K, w); break;
+      case MOE_W_BF16: weights8<MOE_W_BF16>(l.W[side], l.s[side], n, c, l.K, w); break;
+      case MOE_W_INT8_ROW: weights8<MOE_W_INT8_ROW>(l.W[side], l.s[side], n, c, l.K, w); break;
+      case MOE_W_INT4_B32: weights8<MOE_W_INT4_B32>(l.W[side], l.s[side], n, c, l.K, w); break;
+      default: weights8<MOE_W_INT4_B128>(l.W[side], l.s[side], n, c, l.K, w);
+    }
+    const size_t at = (size_t)m * l.ldx + c;
+    if (a.xfmt == MOE_X_F32) token8<MOE_X_F32>(l.x, at, c + 4 < l.K, x);
+    else token8<MOE_X_BF16>(l.x, at, true, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc = fmaf(w[j], x[j], acc);
+  }
+  return acc;
+}
+
+// The NaNs among 16 columns of the warp's 32 tokens again; the whole warp calls it.  Rare and slow:
+// 1,999 tokens of 9,216 columns with an infinity each, 2,304 outputs, take 72 ms where finite ones
+// take 0.5 (a token that holds a NaN itself is left as it is).
+template <bool GATED>
+__device__ __noinline__ void again16(const TcArgs& a, int m, int n0, uint32_t (&v)[16], uint32_t (&u)[16]) {
+  const int lane = lane_id();
+  uint32_t looked = 0, lost = 0;  // tokens looked through, and those of them that hold a NaN
+#pragma unroll 1
+  for (int i = 0; i < (GATED ? 32 : 16); ++i) {
+    const int side = i >> 4, j = i & 15;
+    const float now = __uint_as_float(side ? u[j] : v[j]);
+    uint32_t who = __ballot_sync(0xFFFFFFFFu, now != now && m < a.l.M && n0 + j < a.l.N);
+#pragma unroll 1
+    for (; who; who &= who - 1) {
+      const int r = __ffs(who) - 1, row = m - lane + r;
+      if (!(looked >> r & 1u)) {
+        bool nan = false;
+        for (int c = lane; c < a.l.K; c += 32) {
+          const size_t at = (size_t)row * a.l.ldx + c;
+          const float x = a.xfmt == MOE_X_F32 ? static_cast<const float*>(a.l.x)[at]
+                                              : bf16_to_f32(static_cast<const uint16_t*>(a.l.x)[at]);
+          nan |= x != x;
+        }
+        looked |= 1u << r;
+        lost |= (uint32_t)__any_sync(0xFFFFFFFFu, nan) << r;
+      }
+      if (lost >> r & 1u) continue;
+      float sum = sum_again(a, side, row, n0 + j, 8 * lane, 256);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
+      if (lane == r) (side ? u[j] : v[j]) = __float_as_uint(sum);
+    }
+  }
 }
 
 // The epilogue's code is kept short on purpose: a tile passes through it once, and its way into the
@@ -459,6 +522,19 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           if (GATED) tmem_ld16(at + kTileN / 2 + c, u);
           tmem_ld_wait();
         }
+        if (a.again && a.splits == 1) {
+          float nan = 0.f;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) nan += __uint_as_float(v[j]) + (GATED ? __uint_as_float(u[j]) : 0.f);
+          if (__any_sync(0xFFFFFFFFu, nan != nan)) {
+            uint32_t v2[16], u2[16];  // the call's own: v and u stay in registers
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v2[j] = v[j], u2[j] = GATED ? u[j] : 0u;
+            again16<GATED>(a, m, c_first + c, v2, u2);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = v2[j], u[j] = u2[j];
+          }
+        }
         float* turn = reinterpret_cast<float*>(smem + kStages * kStage + 512 + (w - 4) * kTurn);
         if constexpr (SEG) output16_call<GATED>(a, tl.split, m, c_first + c, v, u, turn);
         else output16<GATED>(a, tl.split, m, c_first + c, v, u, turn);
@@ -496,6 +572,14 @@ __global__ void __launch_bounds__(256) linear_sum_kernel(const __grid_constant__
       if (parts == 2) {
         const float4 q = *reinterpret_cast<const float4*>(a.partial + (((size_t)s * 2 + 1) * l.M + m) * a.np + c);
         u[0] += q.x, u[1] += q.y, u[2] += q.z, u[3] += q.w;
+      }
+    }
+    const float nan = v[0] + v[1] + v[2] + v[3] + u[0] + u[1] + u[2] + u[3];
+    if (a.again && nan != nan) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (v[j] != v[j] && c + j < l.N) v[j] = sum_again(a, 0, m, c + j, 0, 8);
+        if (u[j] != u[j] && c + j < l.N) u[j] = sum_again(a, 1, m, c + j, 0, 8);
       }
     }
 #pragma unroll
@@ -748,6 +832,7 @@ static TcArgs tc_args(const moe_linear_desc& d, const LinearArgs& a, const TcLay
   p.row_scales = d.wfmt == MOE_W_INT8_ROW;
   p.mt = t.mt, p.nt = t.nt, p.splits = t.splits, p.ksteps = t.ksteps, p.segment = t.segment;
   p.xparts = t.xparts, p.wparts = t.wparts, p.np = t.np;
+  p.xfmt = d.xfmt, p.wfmt = d.wfmt, p.again = t.xparts > 1 || t.wparts > 1;
   const int yb = d.yfmt == MOE_X_F32 ? 4 : 2;
   auto pieces = [&](const void* q, long long ld) { return reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld * yb % 16 == 0; };
   p.vec = pieces(a.y, a.ldy) && (!a.residual || pieces(a.residual, a.ldr));

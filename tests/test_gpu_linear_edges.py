@@ -1,0 +1,51 @@
+"""The dense product where arithmetic ends: infinities, sums far below zero, the last bits of fp32
+operands, long reductions."""
+import pytest
+import torch
+
+import mixture_experts_layer_31_b200 as moe
+import ops_ref as ref
+from test_gpu_linear import Product
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _clear_flags():
+    moe.moe_device_flags(clear=True)
+    yield
+    assert moe.moe_device_flags(clear=True) == 0
+
+
+# K, N, M: the reduction split over several CTAs (few columns, more columns); one accumulator;
+# several drained segments
+SPLIT, LONG_SPLIT, WHOLE, SEGMENTS = (256, 96, 50), (2048, 96, 50), (128, 1100, 2500), (1664, 1100, 2500)
+
+
+@pytest.mark.parametrize("wfmt,xfmt,yfmt,gated", [("f32", "f32", "f32", False), ("f32", "f32", "bf16", True),
+                                                  ("f32", "bf16", "f32", False), ("bf16", "f32", "f32", False),
+                                                  ("int8", "f32", "f32", False), ("int4", "f32", "f32", False),
+                                                  ("int4", "bf16", "f32", False), ("int4", "bf16", "bf16", True),
+                                                  ("int4b128", "bf16", "bf16", True)])
+@pytest.mark.parametrize("K,N,M", [SPLIT, LONG_SPLIT, WHOLE, SEGMENTS])
+def test_infinities_in_products_of_parts(wfmt, xfmt, yfmt, gated, K, N, M):
+    """Operands that are multiplied in several bf16 parts: an infinity gives the signed infinity that
+    the formula gives, and NaN only where that does (0 times infinity, infinities of both signs)."""
+    p = Product(K, N, wfmt, xfmt, yfmt=yfmt, gated=gated)
+    x = p.x(M)
+    x[1, 3], x[M // 2, K - 1], x[M - 1, 0] = float("inf"), float("-inf"), float("nan")
+    x[M - 2, 5], x[M - 2, 70] = float("inf"), float("-inf")
+    if wfmt in ("f32", "bf16"):
+        at = [(0, "W", 7, float("inf")), (N - 1, "W", 64, float("-inf"))] + ([(N // 2, "Wu", 9, float("-inf"))] if gated else [])
+        for n, which, k, v in at:
+            getattr(p, which)[n, k] = v
+            p.dev.tensors["W" if which == "W" else "W_up"][n, k] = v
+    y = p.dev(x.cuda()).cpu()
+    rows = torch.tensor(sorted({0, 1, 2, M // 2, M - 3, M - 2, M - 1}))
+    want, bound = ref.linear(x[rows], p.W, None, (p.Wu, None) if gated else None, "none", None, p.y_dtype, wfmt, 2 if gated else 0)
+    got = y[rows].double()
+    assert torch.equal(got.isnan(), want.isnan())
+    inf = want.isinf()
+    assert bool(inf.any()) and torch.equal(got[inf], want[inf])
+    fine = want.isfinite()
+    ref.check(got[fine], want[fine], bound[fine])
