@@ -209,14 +209,16 @@ __device__ __noinline__ void again16(const TcArgs& a, int m, int n0, uint32_t (&
 // instruction cache shows (with every activation inlined for every column it took 17 us before
 // the first tile was stored, whatever the reduction's length).
 
-// the activation of 16 sums: v / (1 + exp(-z)), z = v (SiLU) or twice the tanh-GELU's argument
+// The activation of 16 sums: v / (1 + exp(-z)), z = v (SiLU) or twice the tanh-GELU's argument.  Far
+// below zero the exponential is infinite and nothing may be left of v, however large: FAST
+// multiplies v with a reciprocal that has gone to 0 by then.
 template <bool FAST>
 __device__ __forceinline__ void activate16(float (&v)[16], int act) {
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
     const float z = act == MOE_ACT_SILU ? v[j] : 2.0f * gelu_tanh_z(v[j]);
     // FAST, for bf16 outputs: a few units in the last place of fp32
-    if (FAST) v[j] = __fdividef(v[j], 1.0f + __expf(fminf(-z, 80.0f)));
+    if (FAST) v[j] *= __fdividef(1.0f, 1.0f + __expf(-z));
     else v[j] = v[j] / (1.0f + expf(-z));
   }
 }

@@ -49,3 +49,31 @@ def test_infinities_in_products_of_parts(wfmt, xfmt, yfmt, gated, K, N, M):
     assert bool(inf.any()) and torch.equal(got[inf], want[inf])
     fine = want.isfinite()
     ref.check(got[fine], want[fine], bound[fine])
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("yfmt", ["bf16", "f32"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("K,M", [(256, 8), (256, 100), (2048, 100)])
+def test_activations_of_sums_far_below_zero(act, yfmt, gated, K, M):
+    """Both activations are below |v| exp(-|v|) 2^-126 from v = -200 down, whatever rounding did to
+    v: nothing is left of it beside the residual.  The largest v are their own activation."""
+    low = [-200.0, -1e4, -1e30, -1e36, -3e38, torch.finfo(torch.bfloat16).min, torch.finfo(torch.float32).min]
+    high = [3e4, 1e30, 3e38]
+    p = Product(K, 96, "bf16", yfmt=yfmt, act=act, gated=gated, bias=True)
+    for j, v in enumerate(low + high):
+        p.b[5 * j] = v
+        p.dev.tensors["b"][5 * j] = v
+    p.W[5 * torch.arange(len(low))] *= 0.25  # products far smaller than 200
+    p.dev.tensors["W"][5 * torch.arange(len(low))] *= 0.25
+    x, r = p.x(M), p.residual(M)
+    y = p.dev(x.cuda(), residual=r.cuda()).cpu()
+    at = 5 * torch.arange(len(low))
+    assert bool((x.double() @ p.W[at].T).abs().max() < 60)
+    zero = p.dev(x.cuda()).cpu()[:, at].double()
+    assert bool((zero.abs() <= ref.TINY).all())
+    assert torch.equal(y[:, at], r[:, at])
+    if not gated:
+        at = 5 * (len(low) + torch.arange(len(high)))
+        want = (x.double() @ p.W[at].T + p.b[at])
+        ref.check(y[:, at], want, (2 * ref.HALF[p.y_dtype] + 2.0 ** -20) * want.abs() + 10)
