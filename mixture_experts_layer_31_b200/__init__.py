@@ -326,6 +326,36 @@ def _capturing(torch) -> bool:
     return torch._C._cuda_isCurrentStreamCapturing()
 
 
+class _Workspaces(dict):
+    """Workspaces by stream.  Calls on one stream run in order and share one; a call is several
+    launches, which have to follow one another there, so that host threads take turns."""
+
+    def __init__(self):
+        super().__init__()
+        self._turns = {}
+
+    def turn(self, stream: int):
+        """The lock to hold over the workspace's look-up and the call."""
+        lock = self._turns.get(stream)
+        return lock if lock is not None else self._turns.setdefault(stream, threading.Lock())
+
+    def release(self):
+        for stream in list(self):
+            with self.turn(stream):
+                self.pop(stream, None)
+
+
+_linear_workspaces = {}  # by device, for all Linear objects
+
+
+def release_workspaces() -> None:
+    """Give the workspaces that Linear objects share (for each stream the largest that a call
+    needed) back to PyTorch's allocator; later calls allocate anew.  Captured calls are not
+    concerned: theirs live in their graph's memory."""
+    for kept in list(_linear_workspaces.values()):
+        kept.release()
+
+
 class MoELayer:
     """Device-resident layer: holds the weights as torch CUDA tensors, a reusable
     workspace, and calls moe_route / moe_forward on the current torch stream."""
@@ -369,8 +399,7 @@ class MoELayer:
             self.shared = sh
         self._bws = None
         self._bws_T = -1
-        self._few_ws = {}
-        self._few_lock = threading.Lock()
+        self._few_ws = _Workspaces()
 
     @property
     def x_dtype(self):
@@ -492,7 +521,7 @@ class MoELayer:
                      "residual must be a contiguous %s tensor [%d, %d] on x's device" % (dtype, T, H))
             r = residual.data_ptr()
         stream = _raw_stream(torch, device)
-        with self._few_lock:  # the call's launches must follow one another on the stream
+        with self._few_ws.turn(stream):
             ws = self.few_workspace(T, stream)
             st = lib().moe_few_forward(ctypes.byref(d), None if self.shared is None else ctypes.byref(self.shared),
                                        x.data_ptr(), T, idx.data_ptr(), w.data_ptr(), r, y.data_ptr(), ws.data_ptr(),
@@ -512,9 +541,10 @@ class MoELayer:
 
 class Linear:
     """Device-resident dense product y = act(W x + b) [* (W_up x + b_up)] [+ residual]
-    (moe_linear): holds the weights as torch CUDA tensors and a reusable workspace, and
-    runs on the current torch stream.  W, W_up [N, K] in the storage format wfmt, scales
-    s, s_up and fp32 biases b, b_up as include/moe.h lays them out; yfmt defaults to xfmt."""
+    (moe_linear): holds the weights as torch CUDA tensors and runs on the current torch
+    stream.  W, W_up [N, K] in the storage format wfmt, scales s, s_up and fp32 biases b,
+    b_up as include/moe.h lays them out; yfmt defaults to xfmt.
+    The workspaces belong to the streams, not to the object: release_workspaces()."""
 
     def __init__(self, *, K, N, wfmt, xfmt, W, s=None, b=None, W_up=None, s_up=None, b_up=None, act="none", yfmt=None,
                  device="cuda"):
@@ -537,20 +567,22 @@ class Linear:
         self.desc = d
         self.x_dtype = torch.bfloat16 if d.xfmt == MOE_X_BF16 else torch.float32
         self.y_dtype = torch.bfloat16 if d.yfmt == MOE_X_BF16 else torch.float32
-        self._ws = {}
+        self._ws = _linear_workspaces.setdefault(self.tensors["W"].device, _Workspaces())
         self._need = {}  # workspace bytes by M
-        self._lock = threading.Lock()
 
     def workspace(self, M: int, stream: int = 0):
-        """The workspace of the calls on one stream (they run in order and share it, and one host
-        thread at a time puts its launches there).  A call that is being captured gets one of
-        its own, which lives in its graph's memory."""
+        """The workspace of the products on one stream (they run in order and share it, those of other
+        Linear objects too; one host thread at a time puts its launches there).  A call that is
+        being captured gets one of its own, which lives in its graph's memory."""
         n = self._need.get(M)
         if n is None:
             n = self._need[M] = moe_linear_workspace_size(self.desc, M)
-        ws = self._ws.get(stream)
         capturing = _capturing(self.torch)
-        if capturing or ws is None or ws.numel() < n:
+        ws = None if capturing else self._ws.get(stream)
+        if ws is None or ws.numel() < n:
+            if not capturing:
+                ws = None  # the smaller one goes first
+                self._ws.pop(stream, None)
             ws = self.torch.empty(max(n, 256), dtype=self.torch.uint8, device=self.tensors["W"].device)
             if not capturing:
                 self._ws[stream] = ws
@@ -559,7 +591,7 @@ class Linear:
     def __call__(self, x, residual=None, y=None):
         """x [M, K], rows contiguous but any (16-byte) distance apart; residual and y [M, N]
         with contiguous rows; y may be residual itself.  Calls on one stream share a workspace
-        that the object keeps; a captured call has one in its graph's memory."""
+        that is kept; a captured call has one in its graph's memory."""
         torch, d, device = self.torch, self.desc, self.tensors["W"].device
         K, N, dtype = d.K, d.N, self.y_dtype
         M = x.shape[0]
@@ -579,7 +611,7 @@ class Linear:
                      "residual must be a %s tensor [%d, %d] with contiguous rows on x's device" % (dtype, M, N))
             r, ldr = residual.data_ptr(), residual.stride(0) if M > 1 else N
         stream = _raw_stream(torch, device)
-        with self._lock:  # the call's launches must follow one another on the stream
+        with self._ws.turn(stream):
             ws = self.workspace(M, stream)
             st = lib().moe_linear(ctypes.byref(d), x.data_ptr(), x.stride(0) if M > 1 else K, M, r, ldr, y.data_ptr(),
                                   y.stride(0) if M > 1 else N, ws.data_ptr(), ws.numel(), stream)

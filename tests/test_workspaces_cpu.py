@@ -87,3 +87,80 @@ def test_threads_take_turns_with_a_workspace(calls, make, rows):
     for t in threads:
         t.join()
     assert len(calls.seen) == 15 and calls.overlaps == 0
+
+
+@pytest.mark.parametrize("make,rows", [(_layer, 3), (_linear, 40)])
+def test_threads_on_streams_of_their_own_do_not_wait_for_one_another(calls, monkeypatch, make, rows):
+    """While one thread is inside a call on its stream, another's call on another stream goes through."""
+    _, call = make()
+    inside, go_on = threading.Event(), threading.Event()
+    mine = threading.local()
+    monkeypatch.setattr(moe, "_raw_stream", lambda torch, device: getattr(mine, "stream", 7))
+    plain = calls._call
+
+    def waiting(ws, n, stream):
+        if stream == 8:
+            inside.set()
+            assert go_on.wait(20)
+        return plain(ws, n, stream)
+
+    calls._call = waiting
+
+    def other():
+        mine.stream = 8
+        call(rows)
+
+    t = threading.Thread(target=other)
+    t.start()
+    assert inside.wait(20)
+    free = threading.Thread(target=call, args=(rows,))
+    free.start()
+    free.join(10)
+    done = not free.is_alive()
+    go_on.set()
+    t.join()
+    free.join()
+    assert done and len({ws for ws, _, _ in calls.seen}) == 2
+
+
+def test_products_share_a_workspace_for_each_stream(calls):
+    """A workspace can hold the whole widened matrix: many objects keep the largest one, not one each."""
+    moe.release_workspaces()
+    (a, call_a), (b, call_b) = _linear(), _linear(K=256, N=40)
+    call_b(40)
+    call_a(40)
+    call_b(20)
+    assert len({ws for ws, _, _ in calls.seen}) == 1
+    assert [n for _, n, _ in calls.seen] == 3 * [moe.moe_linear_workspace_size(b.desc, 40)]
+    calls.stream = 8
+    call_a(40)
+    assert calls.seen[-1][0] != calls.seen[0][0]
+    calls.stream = 7
+    call_b(900)  # more than there is: replaced for all of them
+    call_a(40)
+    assert calls.seen[-1][:2] == calls.seen[-2][:2] and calls.seen[-1][1] >= moe.moe_linear_workspace_size(b.desc, 900)
+    assert len(a._ws) == 2
+    moe.release_workspaces()
+    assert len(a._ws) == 0 and len(b._ws) == 0
+    call_a(40)
+    assert calls.seen[-1][1] == max(256, moe.moe_linear_workspace_size(a.desc, 40))
+    moe.release_workspaces()
+
+
+def test_threads_take_turns_with_a_workspace_of_several_products(calls):
+    calls.pause = 0.002
+    some = [_linear()[1], _linear(K=256)[1]]
+    start = threading.Barrier(4)
+
+    def work(call):
+        start.wait()
+        for _ in range(5):
+            call(40)
+
+    threads = [threading.Thread(target=work, args=(some[n % 2],)) for n in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(calls.seen) == 20 and calls.overlaps == 0
+    moe.release_workspaces()
