@@ -317,6 +317,27 @@ def _fits(t, dtype, rows: int, cols: int, device) -> bool:
             and (cols == 1 or t.stride(1) == 1) and t.device == device)
 
 
+def _require_values(name: str, t, dtypes, n: int):
+    """A kernel reads n values of the dtypes' size at t: another tensor would be read out of range."""
+    _require(t is None or (str(t.dtype).split(".")[-1] in dtypes and t.numel() == n),
+             "%s must hold %d values of %s (got %s %s)" % (name, n, " or ".join(dtypes), tuple(t.shape) if t is not None else "",
+                                                           t.dtype if t is not None else ""))
+
+
+def _require_stored(name: str, W, s, wfmt: int, rows: int, cols: int):
+    """Stored weights [rows, cols] and, where the format has them, their scales."""
+    if wfmt == MOE_W_F32:
+        _require_values("W" + name, W, ("float32",), rows * cols)
+    elif wfmt == MOE_W_BF16:
+        _require_values("W" + name, W, ("bfloat16", "int16", "uint16"), rows * cols)
+    elif wfmt == MOE_W_INT8_ROW:
+        _require_values("W" + name, W, ("int8", "uint8"), rows * cols)
+        _require_values("s" + name, s, ("float32",), rows)
+    elif wfmt in (MOE_W_INT4_B32, MOE_W_INT4_B128):
+        _require_values("W" + name, W, ("uint8", "int8"), rows * cols // 2)
+        _require_values("s" + name, s, ("float32",), rows * cols // (32 if wfmt == MOE_W_INT4_B32 else 128))
+
+
 def _raw_stream(torch, device) -> int:
     """The current stream of a CUDA device, as the library takes it."""
     return torch._C._cuda_getCurrentRawStream(device.index)
@@ -400,6 +421,7 @@ class MoELayer:
         self._bws = None
         self._bws_T = -1
         self._few_ws = _Workspaces()
+        self._few_checked = False
 
     @property
     def x_dtype(self):
@@ -494,12 +516,28 @@ class MoELayer:
                 self._few_ws[stream] = ws
         return ws[1]
 
+    def _check_few_tensors(self):
+        """The layer's tensors have the sizes that its description gives."""
+        d, t = self.desc, self.tensors
+        _require_values("W_r", t["W_r"], ("float32",), d.E * d.H)
+        _require_values("b", t["b"], ("float32",), d.E)
+        _require_values("expert_mask", t["expert_mask"], ("uint8", "int8", "bool"), d.E)
+        for part, cols, rows in (("_gate", d.H, d.I), ("_up", d.H, d.I), ("_down", d.I, d.H)):
+            _require_stored(part, t["W" + part], t["s" + part], d.wfmt, d.E * rows, cols)
+        if self.shared is not None:
+            t, I = self.shared_tensors, self.shared.I
+            for part, cols, rows in (("_gate", d.H, I), ("_up", d.H, I), ("_down", I, d.H)):
+                _require_stored(part, t["W" + part], t["s" + part], self.shared.wfmt, rows, cols)
+        self._few_checked = True
+
     def few(self, x, residual=None, out=None):
         """The whole layer for up to MOE_FEW_MAX_TOKENS tokens in two launches (moe_few_forward):
         route, routed experts, the shared expert (if the layer has one) and residual (if
         given, [T, H] in x's dtype).  x [T, H] contiguous; returns (y, idx, w), written into
         `out` = (y, idx, w) if given (y may be residual itself).  Calls on one stream share a
         workspace that the layer keeps; a captured call has one in its graph's memory."""
+        if not self._few_checked:
+            self._check_few_tensors()
         torch, d, device = self.torch, self.desc, self.tensors["W_r"].device
         H, k, dtype = d.H, d.k, self.x_dtype
         T = x.shape[0]
@@ -564,6 +602,11 @@ class Linear:
         for name, a in (("W", W), ("s", s), ("b", b), ("W_up", W_up), ("s_up", s_up), ("b_up", b_up)):
             t = self.tensors[name] = _device_tensor(torch, a, self.device)
             setattr(d, name, None if t is None else t.data_ptr())
+        t = self.tensors
+        _require(t["W"] is not None, "W is missing")
+        for side in ("", "_up"):
+            _require_stored(side, t["W" + side], t["s" + side], d.wfmt, d.N, d.K)
+            _require_values("b" + side, t["b" + side], ("float32",), d.N)
         self.desc = d
         self.x_dtype = torch.bfloat16 if d.xfmt == MOE_X_BF16 else torch.float32
         self.y_dtype = torch.bfloat16 if d.yfmt == MOE_X_BF16 else torch.float32

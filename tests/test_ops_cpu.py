@@ -151,3 +151,55 @@ def test_wrappers_refuse_tensors_of_another_place_or_shape():
         with pytest.raises(moe.MoeError) as ei:
             lin(x)
         assert ei.value.status == INVALID
+
+
+def _linear_tensors(**kw):
+    torch = pytest.importorskip("torch")
+    N, K = 6, 256
+    t = dict(f32=dict(W=torch.zeros(N, K)), bf16=dict(W=torch.zeros(N, K, dtype=torch.bfloat16)),
+             int8=dict(W=torch.zeros(N, K, dtype=torch.int8), s=torch.zeros(N)),
+             int4=dict(W=torch.zeros(N, K // 2, dtype=torch.uint8), s=torch.zeros(N, K // 32)),
+             int4b128=dict(W=torch.zeros(N, K // 2, dtype=torch.uint8), s=torch.zeros(N, K // 128)))[kw.pop("wfmt")]
+    return dict(t, **kw)
+
+
+@pytest.mark.parametrize("wfmt", ["f32", "bf16", "int8", "int4", "int4b128"])
+def test_linear_refuses_tensors_that_its_kernels_would_read_out_of_range(wfmt):
+    torch = pytest.importorskip("torch")
+    make = lambda **kw: moe.Linear(K=256, N=6, wfmt=wfmt, xfmt="bf16", device="cpu", **_linear_tensors(wfmt=wfmt, **kw))
+    good = _linear_tensors(wfmt=wfmt)
+    make(b=torch.zeros(6), W_up=good["W"].clone(), s_up=good.get("s"), b_up=torch.zeros(6))
+    bad = [dict(W=good["W"][:5]), dict(W=good["W"][:, :-1]), dict(W=good["W"].to(torch.float64)), dict(W=None),
+           dict(W_up=good["W"][:5], s_up=good.get("s")), dict(b=torch.zeros(5)), dict(b=torch.zeros(6, dtype=torch.bfloat16)),
+           dict(W_up=good["W"], s_up=good.get("s"), b_up=torch.zeros(12))]
+    if "s" in good:
+        bad += [dict(s=good["s"][:5]), dict(s=good["s"].to(torch.float16)), dict(W_up=good["W"], s_up=good["s"][1:])]
+    for kw in bad:
+        with pytest.raises(moe.MoeError) as ei:
+            make(**kw)
+        assert ei.value.status == INVALID
+
+
+@pytest.mark.parametrize("bad", [None, "W_r", "b", "expert_mask", "W_gate", "W_up", "W_down", "s_gate", "s_up", "s_down", "Ws_gate",
+                                 "Ws_up", "Ws_down", "ss_gate", "ss_up", "ss_down"])
+@pytest.mark.parametrize("wfmt", ["f32", "bf16", "int8", "int4", "int4b128"])
+def test_few_refuses_tensors_that_its_kernels_would_read_out_of_range(wfmt, bad):
+    torch = pytest.importorskip("torch")
+    H, I, E, Is = 256, 128, 4, 128
+    kw = dict(W_r=torch.zeros(E, H), b=torch.zeros(E), expert_mask=torch.ones(E, dtype=torch.uint8))
+    for prefix, lead, width in (("", (E,), I), ("s", (), Is)):
+        for part, r, c in (("gate", width, H), ("up", width, H), ("down", H, width)):
+            dtype, n, s = {"f32": (torch.float32, c, None), "bf16": (torch.bfloat16, c, None), "int8": (torch.int8, c, ()),
+                           "int4": (torch.uint8, c // 2, (c // 32,)), "int4b128": (torch.uint8, c // 2, (c // 128,))}[wfmt]
+            kw["W%s_%s" % (prefix, part)] = torch.zeros(lead + (r, n), dtype=dtype)
+            kw["s%s_%s" % (prefix, part)] = None if s is None else torch.zeros(lead + (r,) + s)
+    if bad is not None and kw[bad] is None:
+        return  # the format has no scales
+    if bad is not None:
+        kw[bad] = kw[bad][:-1]
+    x = torch.zeros(2, H, dtype=torch.bfloat16)
+    layer = moe.MoELayer(H=H, I=I, E=E, k=2, router="sigmoid", scale=1.0, wfmt=wfmt, xfmt="bf16", I_s=Is, device="cpu", **kw)
+    with pytest.raises(moe.MoeError) as ei:
+        layer.few(x)
+    assert ei.value.status == INVALID
+    assert ("must hold" in str(ei.value)) == (bad is not None)  # else it is the place of x
