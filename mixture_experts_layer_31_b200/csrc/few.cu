@@ -4,15 +4,18 @@
 //                softmax router) and the scores, in 64 bits: two neighbouring keys of the
 //                border between the k-th and the next expert can lie closer than an fp32
 //                sum resolves, and at a few tokens the 64-bit sums cost nothing that shows.
-//   few_layer    every CTA picks the top k itself (the keys are a few KB, so this is cheaper
-//                than another launch), then claims work units from a counter:
-//                first the gate/up rows  h[p, i] = act(W_gate x)_i (W_up x)_i  of every
-//                (token, slot) pair p and of the shared expert, then the rows
+//   the layer    every CTA picks the top k itself (the keys are a few KB, so this is cheaper
+//                than another launch), then takes its share first of the gate/up rows
+//                h[p, i] = act(W_gate x)_i (W_up x)_i  of every (token, slot) pair p and
+//                of the shared expert, then of the rows
 //                y[t, r] = sum_j w[t, j] (W_down h[t, j])_r + shared + residual.
-// The down units wait until every gate/up unit is done.  Units are claimed in order and a
-// CTA finishes its claims in order, so the units waited for are always held by CTAs that
-// are running and do not wait themselves: the wait ends however many CTAs are resident and
-// whatever else runs on the GPU.  It is bounded in time all the same (MOE_FLAG_TIMEOUT).
+// Two kernels have the second part: few_stream (bf16 tokens on bf16, int8 or int4 weights) deals its
+// units out as lists, one per CTA, which another CTA may take over; few_layer (fp32 tokens or
+// weights) claims them from a counter.  In both, what is waited for between the two parts is
+// always held by CTAs that are running and do not wait themselves -- few_layer's claims are
+// made and finished in order, few_stream's lists are started by their CTA or taken over -- so
+// the wait ends however many CTAs are resident and whatever else runs on the GPU.  It is
+// bounded in time all the same (MOE_FLAG_TIMEOUT).
 // The router launch zeroes the counters, so the workspace needs no initial state.
 #include <algorithm>
 
@@ -156,7 +159,7 @@ struct FewArgs {
   // lie: [0] routed gate/up, [1] routed down, [2], [3] shared
   uint8_t boxed[4];
   int team, down_team;  // warps that share a gate/up unit, a down entry
-  uint32_t* counters; // [0] claimed units, [kFewDone] finished gate/up units
+  uint32_t* counters; // few_layer: claimed units, [kFewDone] finished gate/up units; few_stream: CTAs, lists
   int32_t* idx;
   float* w;
   void* y;
@@ -905,6 +908,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         while (b < grid && (*reinterpret_cast<volatile uint32_t*>(&a.counters[kFewOwner + b]) != 0 ||
                             atomicExch(&a.counters[kFewOwner + b], 1u) != 0))
           ++b;
+        if (b < grid) atomicAdd(&a.counters[kFewTakenOver], 1u);
         sh.adopted = b < grid ? b : -1;
       }
       __syncthreads();

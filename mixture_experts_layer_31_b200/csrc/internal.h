@@ -205,8 +205,10 @@ cudaError_t launch_expert_counts(const int32_t* idx, int64_t n, int E, uint64_t*
 cudaError_t launch_combine(const moe_desc& d, const int32_t* idx, int T, const void* yp, bool yp_bf16, void* y,
                            cudaStream_t s, const float* ys = nullptr, const void* residual = nullptr);
 // ---- the layer for a few tokens (two launches) ----
-// counters at the start of its workspace: [0] claimed units or started CTAs, [kFewDone] finished
-// gate/up units or lists, each in a 128-byte line of its own, then the lists' owners
+// counters at the start of its workspace: [0] claimed units or started CTAs, [kFewTakenOver] lists
+// that a CTA took over from one that had not started (read by tests alone), [kFewDone] finished
+// gate/up units or lists, in a 128-byte line of its own, then the lists' owners
+constexpr int kFewTakenOver = 1;
 constexpr int kFewDone = 32;
 constexpr int kFewOwner = 64;
 constexpr int kFewLists = 256;

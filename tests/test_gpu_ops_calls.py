@@ -59,3 +59,35 @@ def test_few_from_several_threads_on_one_stream(wfmt, xfmt):
 def test_linear_from_several_threads_on_one_stream(K, N, wfmt, xfmt, M):
     p = Product(K, N, wfmt, xfmt)
     _same_in_threads(lambda x: [p.dev(x)], [p.x(M, 90 + n).cuda() for n in range(4)], 60)
+
+
+@pytest.mark.parametrize("wfmt,T", [("bf16", 2), ("int8", 16), ("int4", 5)])
+def test_lists_of_ctas_that_start_late_are_taken_over(wfmt, T):
+    """A product that holds 80 SMs, with no shared memory left beside it, for a millisecond: calls that
+    start meanwhile have CTAs that cannot, and their lists are taken over; the bits are the
+    same, and the counter in the workspace says that it happened."""
+    layer = Layer(E=64, k=8, H=1024, I=1024, wfmt=wfmt, shared=512)
+    x = layer.x(T, 60).cuda()
+    busy, mine = torch.cuda.Stream(), torch.cuda.Stream()
+    K, N, M = 32768, 1024, 2400  # 40 tiles of the reduction's whole length, each on a pair of SMs
+    W = torch.zeros((N, K), device="cuda")
+    hold = moe.Linear(K=K, N=N, wfmt="f32", xfmt="f32", W=W)
+    a = torch.zeros((M, K), device="cuda")
+    with torch.cuda.stream(mine):
+        want = [t.clone() for t in layer.dev.few(x, residual=x)]
+        taken_over = layer.dev.few_workspace(T, mine.cuda_stream).view(torch.int32)[1]
+    with torch.cuda.stream(busy):
+        hold(a)
+    torch.cuda.synchronize()
+    got, counts = [], []
+    for _ in range(3):
+        with torch.cuda.stream(busy):
+            hold(a)
+        with torch.cuda.stream(mine):
+            for _ in range(30):
+                got.append(layer.dev.few(x, residual=x))
+                counts.append(taken_over.clone())
+    torch.cuda.synchronize()
+    moe.release_workspaces()
+    assert all(torch.equal(p, q) for out in got for p, q in zip(out, want))
+    assert max(int(c) for c in counts) > 0
