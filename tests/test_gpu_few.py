@@ -404,3 +404,22 @@ def test_dense_layer_then_routed_layers():
         want, bound = ref.linear(h.cpu(), dd, None, None, "none", new, torch.bfloat16, "int8")
         ref.check(y, want, bound, "down")
         layer.compare(y.cpu(), z, idx, w, y.cpu(), "routed")
+
+
+@pytest.mark.parametrize("wfmt,xfmt,tol", [("bf16", "bf16", 5e-3), ("int8", "bf16", 5e-3), ("int4", "bf16", 5e-3),
+                                           ("int4b128", "bf16", 5e-3), ("f32", "f32", 1e-5)])
+@pytest.mark.parametrize("T", [1, 16])
+def test_outputs_are_those_of_the_separate_entry_points(wfmt, xfmt, tol, T):
+    """moe_route + moe_forward_block on the tokens that both route alike: no further apart than the
+    other calls' tolerance against 64 bits and this one's bound together."""
+    layer = Layer(shared=128, seed=4, wfmt=wfmt, xfmt=xfmt)
+    x, y, idx, w = layer.run(T, residual=True)
+    r = layer.x(T, 7 + 1000)
+    i2, w2 = layer.dev.route(x.cuda())
+    y2 = layer.dev.block(x.cuda(), i2, w2, residual=r.cuda())
+    same = (i2 == idx).all(1).cpu()
+    assert int(same.sum()) >= T - 1
+    ri, rw = ref.route(x, layer.W_r, layer.b, layer.mask, layer.k, layer.router, layer.scale)
+    want, bound = ref.few(x, ri, rw, layer.experts, layer.act, layer.shared, r)
+    off = (y.cpu().double() - y2.cpu().double())[same].norm()
+    assert float(off) <= tol * float(want[same].norm()) + float(bound[same].norm())

@@ -77,3 +77,65 @@ def test_activations_of_sums_far_below_zero(act, yfmt, gated, K, M):
         at = 5 * (len(low) + torch.arange(len(high)))
         want = (x.double() @ p.W[at].T + p.b[at])
         ref.check(y[:, at], want, (2 * ref.HALF[p.y_dtype] + 2.0 ** -20) * want.abs() + 10)
+
+
+def _all_bits(shape, gen):
+    """fp32 values in [1, 2) whose three bf16 parts are as large as can be: the third is 63 2^-23 in
+    all of them, so that leaving it out shifts every product the same way."""
+    a = torch.randint(0, 127, shape, generator=gen).double()
+    b = torch.randint(128, 251, shape, generator=gen).double() * (2 * torch.randint(0, 2, shape, generator=gen) - 1)
+    v = 1 + a / 128 + b * 2.0 ** -16 + 63 * 2.0 ** -23
+    assert torch.equal(v.float().double(), v)
+    return v.float()
+
+
+def _two_parts(v):
+    h = v.to(torch.bfloat16).float()
+    return (h + (v - h).to(torch.bfloat16).float()).double()
+
+
+@pytest.mark.parametrize("wfmt,xfmt", [("f32", "f32"), ("f32", "bf16"), ("bf16", "f32"), ("int8", "f32")])
+@pytest.mark.parametrize("K", [16, 32])
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** -100])
+@pytest.mark.parametrize("M", [3, 40])
+def test_every_bit_of_fp32_operands(wfmt, xfmt, K, scale, M):
+    """Short reductions, whose worst rounding is smaller than what a third part brings."""
+    gen, N = torch.Generator().manual_seed(K + M), 64
+    x = _all_bits((M, K), gen).to(torch.bfloat16 if xfmt == "bf16" else torch.float32)
+    x, s = x * scale if xfmt == "f32" else x, None
+    if wfmt == "int8":
+        W, s = torch.randint(64, 128, (N, K), generator=gen).to(torch.int8), torch.full((N,), 2.0 ** -6)
+        Wd = W.double() * 2.0 ** -6
+    else:
+        W = _all_bits((N, K), gen).to(torch.bfloat16 if wfmt == "bf16" else torch.float32)
+        W = W * scale if xfmt == "bf16" and scale != 1 else W
+        Wd = W.double()
+    y = moe.Linear(K=K, N=N, wfmt=wfmt, xfmt=xfmt, yfmt="f32", W=W, s=s)(x.cuda())
+    want = x.double() @ Wd.T
+    bound = ref.sum_error(K, x.double().abs() @ Wd.abs().T) + ref.HALF[torch.float32] * want.abs()
+    ref.check(y, want, bound)
+    # the oracle with a part left out is off by more than that everywhere
+    if xfmt == "f32":
+        assert bool(((_two_parts(x) @ Wd.T - want).abs() > bound).all())
+    if wfmt == "f32":
+        assert bool(((x.double() @ _two_parts(W).T - want).abs() > bound).all())
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "f32"])
+def test_long_sums_of_one_sign_are_not_cut_off(fmt):
+    """65,536 positive columns, fp32 output.  An accumulator is drained after 12 steps of 4
+    instructions at full magnitude: were each of these 48 additions cut off by a whole unit of the
+    last place, the sums would come out 48 x 2^-23 too small at most; the drained sums are added
+    with rounding to nearest, whose errors are as often up as down.  4,096 additions in a
+    row that cut off by half a unit each lose 4096 / 2 x 2^-24 = 1.2 x 10^-4."""
+    dtype = torch.bfloat16 if fmt == "bf16" else torch.float32
+    K, N, M = 65536, 1024, 2400  # tiles enough that the reduction is not split
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.empty((M, K), device="cuda").uniform_(1, 2, generator=gen).to(dtype)
+    W = torch.empty((N, K), device="cuda").uniform_(1, 2, generator=gen).to(dtype)
+    y = moe.Linear(K=K, N=N, wfmt=fmt, xfmt=fmt, yfmt="f32", W=W)(x)
+    rows, cols = torch.arange(0, M, 149, device="cuda"), torch.arange(0, N, 31, device="cuda")
+    want = x[rows].double() @ W[cols].double().T
+    off = (y[rows][:, cols].double() - want) / want
+    assert bool(off.abs().max() <= (K + ref.STEPS) * ref.U)
+    assert abs(float(off.mean())) <= 48 * 2.0 ** -23

@@ -91,3 +91,39 @@ def test_lists_of_ctas_that_start_late_are_taken_over(wfmt, T):
     moe.release_workspaces()
     assert all(torch.equal(p, q) for out in got for p, q in zip(out, want))
     assert max(int(c) for c in counts) > 0
+
+
+def test_programmatic_launches_do_not_change_results(tmp_path):
+    """MOE_PDL=1 (read once per process, so in a child process): every first launch of a call may then
+    start while the call before it ends.  Calls one after the other, whose workspaces are the
+    same, give the same bits as in plain stream order."""
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    script = tmp_path / "calls.py"
+    script.write_text(
+        "import sys, torch\n"
+        f"sys.path[:0] = [{os.path.dirname(here)!r}, {here!r}]\n"
+        "import mixture_experts_layer_31_b200 as moe\n"
+        "from test_gpu_few import Layer\n"
+        "from test_gpu_linear import Product\n"
+        "ops = []\n"
+        "for wfmt, xfmt in (('bf16', 'bf16'), ('int8', 'bf16'), ('int4', 'bf16'), ('f32', 'f32')):\n"
+        "    layer = Layer(wfmt=wfmt, xfmt=xfmt, shared=128)\n"
+        "    ops += [(lambda x, f=layer.dev: torch.cat([t.flatten().float() for t in f.few(x, residual=x)]), layer.x(T).cuda())\n"
+        "            for T in (1, 5)]\n"
+        "    product = Product(2048, 96, wfmt, xfmt, bias=True, act='silu')\n"
+        "    ops += [(product.dev, product.x(M).cuda()) for M in (1, 5, 20, 70)]\n"
+        "out = [[f(x) for f, x in ops] for _ in range(20)]\n"
+        "torch.cuda.synchronize()\n"
+        "assert moe.moe_device_flags() == 0\n"
+        "assert all(torch.equal(a, b) for o in out for a, b in zip(o, out[0]))\n"
+        "torch.save([t.cpu() for t in out[0]], sys.argv[1])\n")
+    runs = {}
+    for pdl in ("0", "1"):
+        dst = tmp_path / ("out_%s.pt" % pdl)
+        subprocess.run([sys.executable, str(script), str(dst)], check=True, env=dict(os.environ, MOE_PDL=pdl), timeout=300)
+        runs[pdl] = torch.load(dst)
+    assert len(runs["0"]) == 24
+    assert all(torch.equal(a, b) for a, b in zip(runs["0"], runs["1"]))
