@@ -51,6 +51,24 @@ def test_infinities_in_products_of_parts(wfmt, xfmt, yfmt, gated, K, N, M):
     ref.check(got[fine], want[fine], bound[fine])
 
 
+@pytest.mark.parametrize("wfmt,xfmt,M", [("bf16", "bf16", 5), ("bf16", "bf16", 20), ("bf16", "bf16", 150), ("int8", "bf16", 12),
+                                         ("int8", "bf16", 60), ("int8", "bf16", 150), ("int4", "bf16", 12), ("int4", "bf16", 40),
+                                         ("int4", "bf16", 150), ("int4b128", "bf16", 20), ("f32", "f32", 5), ("bf16", "f32", 16),
+                                         ("int8", "f32", 9), ("int4", "f32", 5), ("f32", "bf16", 16)])
+def test_infinities_in_the_other_forms(wfmt, xfmt, M):
+    p = Product(384, 75, wfmt, xfmt)
+    x = p.x(M)
+    x[1, 3], x[M - 1, 380] = float("inf"), float("-inf")
+    x[M - 2, 5], x[M - 2, 70] = float("inf"), float("-inf")
+    y = p.dev(x.cuda()).cpu().double()
+    want, bound = ref.linear(x, p.W, None, None, "none", None, p.y_dtype, wfmt, 1)
+    assert torch.equal(y.isnan(), want.isnan())
+    inf = want.isinf()
+    assert bool(inf.any()) and torch.equal(y[inf], want[inf])
+    fine = want.isfinite()
+    ref.check(y[fine], want[fine], bound[fine])
+
+
 @pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
 @pytest.mark.parametrize("yfmt", ["bf16", "f32"])
 @pytest.mark.parametrize("gated", [False, True])
