@@ -281,7 +281,8 @@ MOE_API moe_status moe_forward_block(const moe_desc* d, const moe_shared_expert*
  *     call gives the same bits.
  *   - bf16 tokens meet int8 and int4 gate and up weights as integers of 31 bits relative to the
  *     token's largest magnitude: what lies 22 binary places and more below that loses low
- *     bits, and a token that holds an infinity or NaN gives NaN in its whole row of y.
+ *     bits, and a token that holds an infinity or NaN gives NaN in its whole row of y.  So
+ *     does an activation between the projections that overflowed, on int4 down weights.
  *   - d->path is not read.
  * The workspace (moe_few_workspace_size bytes, 256-byte aligned) needs no initial state;
  * calls on one stream may share it, calls that can overlap must not.  A call is two launches:
@@ -320,13 +321,15 @@ MOE_API moe_status moe_few_forward(const moe_desc* d, const moe_shared_expert* s
  *   to their element.  y may be residual itself (same ldr and ldy; each element is read before
  *   it is written, by the same thread) and must not overlap x.  M = 0 does nothing.
  *   Columns between N and ldy, and what lies behind the last row, are not touched.
- * Sums are fp32 (integers where a few bf16 tokens meet int8 or int4 weights: the token is
- * taken as integers of 31 bits relative to its largest magnitude, and one that holds an
- * infinity or NaN gives NaN in its whole row of y).  fp32 weights and tokens are multiplied in
- * fp32, for more tokens in three bf16 parts each that hold every bit of magnitudes from 2^-100
- * up; infinities are infinities there too.  int4 weights are
- * exact for up to 40 tokens (of bf16; 48 where K > 4096) and wherever y is fp32; beyond, with
- * bf16 tokens and bf16 y, each is rounded to bf16 once (gated: kept to 16 bits).
+ * Sums are fp32.  Where up to 8 bf16 tokens meet int8 weights or up to 2 int4 weights they are
+ * integers, the token taken as integers of 31 bits relative to its largest magnitude.  Up to 8
+ * bf16 tokens on int8 or int4 weights, one that holds an infinity or NaN gives NaN in its whole
+ * row of y; all other forms give the infinities that the formula gives.  Sums with codes are
+ * formed before the row's or block's scale: tokens beyond 2^100 may overflow there.
+ * fp32 weights and tokens are multiplied in fp32, for more tokens in three bf16 parts each that
+ * hold every bit of magnitudes from 2^-100 up.  int4 weights are exact for up to 40 tokens (of
+ * bf16; 48 where K > 4096) and wherever y is fp32; beyond, with bf16 tokens and bf16 y, each is
+ * rounded to bf16 once (gated: kept to 16 bits).
  * The workspace is as for moe_forward: moe_linear_workspace_size bytes for this very M (fewer
  * rows may need more; may be 0, then it may be NULL), 256-byte aligned, no initial state
  * needed, shared by the calls of one stream only, and of one host thread at a time (a call is

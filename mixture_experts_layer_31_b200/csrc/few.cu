@@ -410,12 +410,13 @@ __global__ void __launch_bounds__(kFewThreads) few_layer_kernel(const FewArgs a)
 // as y's own rounding.  What is summed together depends on the plan alone, so the same call
 // gives the same bits.
 //
-// Measured, both launches, with what the bytes alone need at the copy rate of 6.55 TB/s:
-//   1 token   bf16, 2,304 wide, 256 experts of 2,048, 8 chosen, shared    55 us   39 us
-//   4 tokens  int8, the same layer                                        98 us   69 us
-//   16 tokens int8, the same layer                                       238 us  194 us
-//   1 token   int4, 2,048 wide, 128 experts of 768, 8 chosen              26 us    4 us
-//   16 tokens int4, the same layer                                       107 us   37 us
+// Measured, both launches among calls on other inputs (ranges: over several GPUs), with what the
+// bytes alone need at the copy rate of 6.55 TB/s:
+//   1 token   bf16, 2,304 wide, 256 experts of 2,048, 8 chosen, shared    55 us       39 us
+//   4 tokens  int8, the same layer                                        97-99 us    69 us
+//   16 tokens int8, the same layer, 160 experts active                   238-245 us  194 us
+//   1 token   int4, 2,048 wide, 128 experts of 768, 8 chosen              26 us        4 us
+//   16 tokens int4, the same layer                                       107-111 us   37 us
 // The first three are bound by HBM behind some 15 us of router, plan, first loads and barrier; one
 // int4 token by those alone.  Sixteen int4 tokens are bound by the instructions of the
 // products (a box of 2 KB takes some 250 of them, at 0.43 per cycle and scheduler with three
@@ -1125,9 +1126,10 @@ cudaError_t launch_stream(FewArgs a, int num_sms, cudaStream_t s) {
   static_assert(smem <= 232448, "the rings do not fit in shared memory");
   // Sharing a unit out costs each warp some hundred instructions of hand-over, which counts where
   // instructions bound the stream; where the units are few, smaller teams leave warps without
-  // work in the last round.  Measured (teams of 12, 3, 1): 1 token bf16 56, 57, 57 us and int4
-  // 27, 28, 38 us; 4 tokens int8 128, 105, 118 us; 16 tokens int8 297, 240, 248 us and int4 138,
-  // 111, 124 us (a step before the present one).  Down teams of 1 where 3 is chosen: within 1%.
+  // work in the last round.  Measured by events after a flush of L2 (teams of 12, 3, 1): 1 token bf16
+  // 68, 68, 70 us and int4 33, 31, 41 us; 4 tokens int8 129, 117, 128 us; 16 tokens int8 298, 242,
+  // 251 us and int4 135, 109, 121 us.  Down teams of 12, 3, 1: 1 token bf16 68, 70, 70 us, 16 tokens
+  // int8 250, 242, 242 us, all others within 1%.
   // The tokens' experts are not known here: expect them to differ.
   const int touched = std::min(a.T * a.k, a.E);
   a.team = (int64_t)touched * (a.I / 16) >= 4LL * 4 * num_sms ? 3 : kWarps;

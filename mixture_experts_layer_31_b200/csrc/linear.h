@@ -27,6 +27,10 @@ struct LinearArgs {
 //   int8   9216 x 2304, 64 tokens 29, 37;  2304 x (9216 + 9216), 48 tokens 49, 52, 64 tokens 62, 54
 //   int4   2304 x (9216 + 9216), 40 tokens 46, 52;  2048 x 4999, 32 tokens 15, 23, 48 tokens 25, 23;
 //          9216 x 2304, 48 tokens 25, 36, 64 tokens 40, 38
+// Ten more shapes from 1024 x 1024 to 768 x 16384 and 16384 x 1024 (by events after a flush of L2, 4 us
+// more than the above): the rule takes the faster form or one within 15% on square ones; short or long
+// reductions cross over sooner.  The worst: 768 x 16384, bf16 32 tokens 25, 17, int8 48 tokens 37, 27,
+// int4 40 tokens 41, 23; 16384 x 1024, bf16 32 tokens 31, 23, int8 64 tokens 47, 31, int4 48 tokens 62, 30.
 inline int linear_stream_tokens(const moe_linear_desc& d) {
   const bool large = (int64_t)d.N * d.K * (d.W_up ? 2 : 1) > 32 << 20;
   if (d.wfmt == MOE_W_INT8_ROW) return large ? 48 : 64;

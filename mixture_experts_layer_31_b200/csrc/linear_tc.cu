@@ -33,14 +33,19 @@
 // weight, as the routed layer's tensor-core path has it: measured against 64 bits 2.2 x 10^-3
 // where y's own rounding alone leaves 1.7 x 10^-3), in two parts where two such projections are
 // multiplied (one part left 2.7 x 10^-3), in three parts where y is fp32.
-// The pass costs 3 bytes or 2.6 per weight, most of it in L2, against 2 M operations per
-// weight.
+// The pass reads 1 byte per weight of int8, 0.5 and the scales of int4, 4 of fp32, and writes 2 for
+// each part (fp32 and int4 for fp32 outputs: 6); the product reads the parts again.  Where they
+// fit L2 (126 MB) with the rest, most of that stays there; larger matrices go through HBM
+// twice more: 229 tokens, 6,272 columns, 12,694 gated outputs, int4 in two parts, 637 MB each way
+// are the larger part of 320 us.
 //
-// Measured: 4,096 tokens, 2,304 columns, 9,216 gated outputs, bf16, 219 us alone (1,586 TFLOP/s, 97%
-// of the rate of a large library product, the tensor pipe 81% busy) and 250 to 290 us in a
-// loop, where the power limit lowers the clock; 1,999 tokens, 9,216 columns, 2,304 outputs,
-// int8, 66 us after a widening pass of 13; 2,048 tokens, 2,304 x 2,304, fp32, 117 us.  L2 is at
-// half its rate meanwhile.
+// Measured: 4,096 tokens, 2,304 columns, 9,216 gated outputs, bf16, one launch by itself under the
+// profiler 219 to 250 us over several GPUs (up to 1,586 TFLOP/s, 97% of the rate of a large
+// library product; the tensor pipe is busy 81% of the cycles on all of them) and 287 to 298 us
+// among other calls, where the power limit lowers the clock; 1,999 tokens, 9,216 columns,
+// 2,304 outputs, int8, 66 to 74 us by itself behind a widening pass of 13, both together 88 to
+// 90 us among other calls; 2,048 tokens, 2,304 x 2,304, fp32, 117 us.  L2 is at half its rate
+// meanwhile.
 #include <cuda.h>
 
 #include <algorithm>
